@@ -15,7 +15,9 @@ NOALLOC_SCRATCH_BYTES = 128 << 20      # MOE_NOALLOC_SCRATCH_BYTES
 RING_MAX_SLOTS = 32
 
 ROUTE_DENSE_I16, ROUTE_DENSE_I32, ROUTE_SPARSE_BOOL = 0, 1, 2
-BF16, FP8E4M3_B128 = 0, 1
+BF16, FP8E4M3_B128, F32, INT4_G128 = 0, 1, 2, 3
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+NORM_MAX_H = 32768
 
 FLAG_CAPACITY, FLAG_OUT_ROWS, FLAG_BAD_EXPERT, FLAG_DUPLICATE = 1, 2, 4, 8
 
@@ -79,6 +81,12 @@ SIGNATURES = [
                                        C.c_int32, _P, _P]),
     ("moe_dispatch_backward", C.c_int, [C.POINTER(MoeHandle), _P, _P, _P, _P, _P]),
     ("moe_combine_backward", C.c_int, [C.POINTER(MoeHandle), _P, _P, C.c_int32, _P, _P, _P]),
+    ("moe_gate", C.c_int, [C.POINTER(MoeHandle), _P, C.c_int32, _P, C.c_int32, C.c_int32, C.c_float, _P, _P, _P]),
+    ("moe_gate_backward", C.c_int, [C.POINTER(MoeHandle), _P, _P, C.c_int32, _P, C.c_int32, C.c_int32, C.c_float, _P,
+                                    _P]),
+    ("moe_layer_norm", C.c_int, [C.c_int32] * 5 + [_P, _P, _P, C.c_float, _P, _P, _P, _P]),
+    ("moe_layer_norm_backward_scratch_bytes", C.c_size_t, [C.c_int32, C.c_int32]),
+    ("moe_layer_norm_backward", C.c_int, [C.c_int32] * 5 + [_P] * 9 + [C.c_size_t, _P]),
 ]
 
 _lib = None

@@ -17,7 +17,10 @@ from . import _abi as A
 _FMT = {"dense_i16": A.ROUTE_DENSE_I16, "dense_i32": A.ROUTE_DENSE_I32, "sparse_bool": A.ROUTE_SPARSE_BOOL}
 _FMT_DTYPES = {A.ROUTE_DENSE_I16: (torch.int16,), A.ROUTE_DENSE_I32: (torch.int32,),
                A.ROUTE_SPARSE_BOOL: (torch.uint8, torch.bool, torch.int8)}
-_DT = {"bf16": A.BF16, "fp8": A.FP8E4M3_B128}
+_DT = {"bf16": A.BF16, "fp8": A.FP8E4M3_B128, "int4": A.INT4_G128}
+_ROW_DT = {torch.bfloat16: A.BF16, torch.float32: A.F32}
+_SCORE = {"softmax": A.GATE_SOFTMAX, "sigmoid": A.GATE_SIGMOID}
+_ROUTING_OUT = {A.ROUTE_DENSE_I16: torch.int16, A.ROUTE_DENSE_I32: torch.int32, A.ROUTE_SPARSE_BOOL: torch.uint8}
 _FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -60,6 +63,101 @@ def assert_no_overflow(flag: torch.Tensor) -> None:
     """Device-side assert that the overflow flag is clear; the host does not
     wait for it (the failure surfaces at the next synchronisation)."""
     torch._assert_async(flag[0] == 0)
+
+
+def _check_rows(t, name, shape, dtypes):
+    _need(t.dtype in dtypes and tuple(t.shape) == shape, f"{name} must be {' or '.join(str(d) for d in dtypes)} "
+          f"{list(shape)}, got {t.dtype} {list(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _check_current_device(**tensors):
+    for name, t in tensors.items():
+        _need(t is None or (t.is_cuda and t.device.index == torch.cuda.current_device()),
+              f"{name} must live on the current GPU")
+
+
+def _check_norm_params(H, **params):
+    """The parameters' common dtype (float32 where there are none)."""
+    kinds = set()
+    for name, p in params.items():
+        if p is not None:
+            _check_rows(p, name, (H,), tuple(_ROW_DT))
+            kinds.add(p.dtype)
+    _need(len(kinds) <= 1, "weight and bias must share their dtype")
+    return _ROW_DT[kinds.pop()] if kinds else A.F32
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, *, out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+               mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None):
+    """Layer norm of rows x [T,H] (bf16 or fp32; weight and bias [H] of one of
+    these types): (out [T,H], mean [T], rstd [T]), the last two fp32, for
+    layer_norm_backward.  ``out`` is of ``out_dtype`` (default: x's)."""
+    _need(x.dim() == 2, "x must be [T,H]")
+    T, H = x.shape
+    _check_rows(x, "x", (T, H), tuple(_ROW_DT))
+    wdt = _check_norm_params(H, weight=weight, bias=bias)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=x.device)
+    _check_rows(out, "out", (T, H), tuple(_ROW_DT) if out_dtype is None else (out_dtype,))
+    if mean is None:
+        mean = torch.empty(T, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check_rows(mean, "mean", (T,), (torch.float32,))
+    _check_rows(rstd, "rstd", (T,), (torch.float32,))
+    _need(out.dtype in _ROW_DT, f"out must be bfloat16 or float32, got {out.dtype}")
+    _check_current_device(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    A.check(A.lib().moe_layer_norm(T, H, _ROW_DT[x.dtype], _ROW_DT[out.dtype], wdt, _ptr(x), _ptr(weight), _ptr(bias),
+                                   float(eps), _ptr(out), _ptr(mean), _ptr(rstd), _stream()), "moe_layer_norm")
+    return out, mean, rstd
+
+
+def layer_norm_backward_scratch_bytes(T: int, H: int) -> int:
+    return int(A.lib().moe_layer_norm_backward_scratch_bytes(int(T), int(H)))
+
+
+def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None,
+                        grad_weight: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None,
+                        scratch: Optional[torch.Tensor] = None, want_params: bool = True):
+    """Gradients of a layer norm: (grad_x [T,H] of x's dtype, grad_weight [H],
+    grad_bias [H]), the last two fp32, or None without ``want_params``.
+    mean and rstd are the forward's."""
+    _need(x.dim() == 2, "x must be [T,H]")
+    T, H = x.shape
+    _check_rows(x, "x", (T, H), tuple(_ROW_DT))
+    _check_rows(grad_y, "grad_y", (T, H), tuple(_ROW_DT))
+    _check_rows(mean, "mean", (T,), (torch.float32,))
+    _check_rows(rstd, "rstd", (T,), (torch.float32,))
+    wdt = _check_norm_params(H, weight=weight)
+    if out is None:
+        out = torch.empty_like(x)
+    _check_rows(out, "out", (T, H), (x.dtype,))
+    if want_params:
+        if grad_weight is None:
+            grad_weight = torch.empty(H, dtype=torch.float32, device=x.device)
+        if grad_bias is None:
+            grad_bias = torch.empty(H, dtype=torch.float32, device=x.device)
+        _check_rows(grad_weight, "grad_weight", (H,), (torch.float32,))
+        _check_rows(grad_bias, "grad_bias", (H,), (torch.float32,))
+        need = layer_norm_backward_scratch_bytes(T, H)
+        _need(need > 0, f"rows of {H} elements are outside 1..{A.NORM_MAX_H}")
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _need(scratch.is_contiguous(), "scratch must be contiguous")
+        _need(scratch.numel() * scratch.element_size() >= need, f"scratch holds fewer than the {need} bytes needed")
+    else:
+        _need(grad_weight is None and grad_bias is None, "grad_weight and grad_bias need want_params")
+    _check_current_device(grad_y=grad_y, x=x, mean=mean, rstd=rstd, weight=weight, out=out, grad_weight=grad_weight,
+                          grad_bias=grad_bias, scratch=scratch)
+    nbytes = 0 if scratch is None else scratch.numel() * scratch.element_size()
+    A.check(A.lib().moe_layer_norm_backward(T, H, _ROW_DT[x.dtype], _ROW_DT[grad_y.dtype], wdt, _ptr(grad_y), _ptr(x),
+                                            _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(out), _ptr(grad_weight),
+                                            _ptr(grad_bias), _ptr(scratch), nbytes, _stream()),
+            "moe_layer_norm_backward")
+    return out, grad_weight, grad_bias
 
 
 class Dispatcher:
@@ -132,6 +230,56 @@ class Dispatcher:
         if T_live is not None:
             self._dev(T_live, "T_live")
             _need(T_live.dtype == torch.int32 and T_live.numel() == 1, "T_live must be one int32")
+
+    # ---- gate --------------------------------------------------------------------
+    def _routing_shape(self):
+        return (self.T, self.E) if self.route_fmt == A.ROUTE_SPARSE_BOOL else (self.T, self.K)
+
+    def _check_gate(self, logits, score):
+        self._dev(logits, "logits")
+        _need(logits.dtype in _ROW_DT and tuple(logits.shape) == (self.T, self.E),
+              f"logits must be bfloat16 or float32 [{self.T}, {self.E}], got {logits.dtype} {tuple(logits.shape)}")
+        _need(score in _SCORE, f"score must be one of {sorted(_SCORE)}, got {score!r}")
+
+    def gate(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, *, score: str = "softmax",
+             normalize: bool = False, scale: float = 1.0, routing: Optional[torch.Tensor] = None,
+             probs: Optional[torch.Tensor] = None):
+        """The top-k experts of each token and their weights from router logits
+        [T,E] (bf16 or fp32): (routing, probs) in this Dispatcher's routing
+        format, as preprocess and dispatch take them.  ``bias`` [E] (fp32)
+        steers the choice only; -inf logits switch experts off."""
+        self._check_gate(logits, score)
+        if bias is not None:
+            self._dev(bias, "bias")
+            _need(bias.dtype == torch.float32 and tuple(bias.shape) == (self.E,), "bias must be float32 [E]")
+        shape = self._routing_shape()
+        if routing is None:
+            routing = torch.empty(shape, dtype=_ROUTING_OUT[self.route_fmt], device=self.device)
+        if probs is None:
+            probs = torch.empty(shape, dtype=torch.float32, device=self.device)
+        self._check_routing(routing, probs, None)
+        _check_current_device(logits=logits)
+        A.check(A.lib().moe_gate(C.byref(self.h), _ptr(logits), _ROW_DT[logits.dtype], _ptr(bias), _SCORE[score],
+                                 1 if normalize else 0, float(scale), _ptr(routing), _ptr(probs), _stream()),
+                "moe_gate")
+        return routing, probs
+
+    def gate_backward(self, grad_probs: torch.Tensor, logits: torch.Tensor, routing: torch.Tensor, *,
+                      score: str = "softmax", normalize: bool = False, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient of the gate's weights (grad_probs, in the routing's shape,
+        as combine_backward gives it) to the logits [T,E], in their dtype."""
+        self._check_gate(logits, score)
+        self._check_routing(routing, grad_probs, None)
+        if out is None:
+            out = torch.empty_like(logits)
+        self._dev(out, "out")
+        _need(out.dtype == logits.dtype and out.shape == logits.shape, "out must be like logits")
+        _check_current_device(logits=logits)
+        A.check(A.lib().moe_gate_backward(C.byref(self.h), _ptr(grad_probs), _ptr(logits), _ROW_DT[logits.dtype],
+                                          _ptr(routing), _SCORE[score], 1 if normalize else 0, float(scale),
+                                          _ptr(out), _stream()), "moe_gate_backward")
+        return out
 
     # ---- calls -------------------------------------------------------------------
     def preprocess(self, routing: torch.Tensor, probs: Optional[torch.Tensor] = None,
@@ -237,8 +385,13 @@ class Dispatcher:
 
     def _check_w1(self, w1: torch.Tensor, w1_scales: Optional[torch.Tensor]):
         """FC1 weights [E, 2F, H] (bf16, or e4m3 codes with [E, 2F/128, H/128]
-        float32 block scales) on this device; returns (F, wdtype)."""
+        float32 block scales, or packed 4-bit codes [E, 2F, H/2] with
+        [E, 2F, H/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w1, "w1")
+        if self._is_int4(w1, w1_scales):
+            _need(w1.shape[0] == self.E and 2 * w1.shape[2] == self.H and w1.shape[1] % 2 == 0 and w1.shape[1] > 0,
+                  f"4-bit w1 must be [E, 2F, H/2] = [{self.E}, 2F, {self.H // 2}], got {tuple(w1.shape)}")
+            return int(w1.shape[1]) // 2, self._check_int4(w1, w1_scales, "w1")
         _need(w1.dim() == 3 and w1.shape[0] == self.E and w1.shape[2] == self.H and w1.shape[1] % 2 == 0
               and w1.shape[1] > 0, f"w1 must be [E, 2F, H] = [{self.E}, 2F, {self.H}], got {tuple(w1.shape)}")
         F = int(w1.shape[1]) // 2
@@ -246,12 +399,34 @@ class Dispatcher:
 
     def _check_w2(self, w2: torch.Tensor, w2_scales: Optional[torch.Tensor]):
         """FC2 weights [E, H, F] (bf16, or e4m3 codes with [E, H/128, F/128]
-        float32 block scales) on this device; returns (F, wdtype)."""
+        float32 block scales, or packed 4-bit codes [E, H, F/2] with
+        [E, H, F/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w2, "w2")
+        if self._is_int4(w2, w2_scales):
+            _need(w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0,
+                  f"4-bit w2 must be [E, H, F/2] = [{self.E}, {self.H}, F/2], got {tuple(w2.shape)}")
+            return 2 * int(w2.shape[2]), self._check_int4(w2, w2_scales, "w2")
         _need(w2.dim() == 3 and w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0,
               f"w2 must be [E, H, F] = [{self.E}, {self.H}, F], got {tuple(w2.shape)}")
         F = int(w2.shape[2])
         return F, self._check_wdtype(w2, w2_scales, "w2", (self.E, self.H // 128, F // 128))
+
+    @staticmethod
+    def _is_int4(w, scales) -> bool:
+        """Byte weights are packed 4-bit codes where every weight row has its
+        own scales; e4m3 codes share a scale among 128 rows."""
+        return (w.dtype == torch.uint8 and w.dim() == 3 and scales is not None and scales.dim() == 3
+                and scales.shape[1] == w.shape[1])
+
+    def _check_int4(self, w, scales, name) -> str:
+        cols = 2 * int(w.shape[2])
+        _need(self.H % 128 == 0 and w.shape[1] % 128 == 0 and cols % 128 == 0,
+              f"4-bit {name} needs dimensions that are multiples of 128")
+        shape = (self.E, int(w.shape[1]), cols // 128)
+        self._dev(scales, f"{name}_scales")
+        _need(scales.dtype == torch.float32 and tuple(scales.shape) == shape,
+              f"{name}_scales must be float32 {shape}, got {scales.dtype} {tuple(scales.shape)}")
+        return "int4"
 
     def _check_wdtype(self, w, scales, name, scale_shape):
         if w.dtype in _FP8_DTYPES:
@@ -282,8 +457,10 @@ class Dispatcher:
                     scratch: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                     perm_scales: Optional[torch.Tensor] = None):
         """Grouped SwiGLU MLP over the permuted rows.  w1 [E,2F,H], w2 [E,H,F]
-        (bf16, or e4m3 codes with 128x128 block scales).  With a handle of fp8
-        payload, perm is e4m3 codes quantised on dispatch plus perm_scales
+        (bf16, or e4m3 codes with 128x128 block scales, or packed 4-bit codes
+        w1 [E,2F,H/2], w2 [E,H,F/2] with scales [E,2F,H/128], [E,H,F/128]: see
+        _check_w1).  With 4-bit weights, rows of ``out`` that hold no kept copy
+        are left as they were.  With a handle of fp8 payload, perm is e4m3 codes quantised on dispatch plus perm_scales
         (fp8 weights only)."""
         F, wdtype = self._check_w1(w1, w1_scales)
         F2, wdtype2 = self._check_w2(w2, w2_scales)
@@ -295,6 +472,8 @@ class Dispatcher:
         if out is None:
             out = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
         self._check_expert_out(out)
+        if wdtype == "int4":
+            _check_current_device(perm=perm)
         A.check(A.lib().moe_grouped_swiglu_mlp(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                                scratch.numel(), _ptr(out), _stream()), "moe_grouped_swiglu_mlp")
@@ -312,6 +491,8 @@ class Dispatcher:
         _need(F2 == F and wdtype2 == wdtype, "w1 and w2 must share the FFN width and dtype")
         self._check_perm(perm, perm_scales)
         self._check_expert_out(out)
+        if wdtype == "int4":
+            _check_current_device(perm=perm)
         A.check(A.lib().moe_grouped_swiglu_mlp_noalloc(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales),
                                                        _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(out),
                                                        _stream()), "moe_grouped_swiglu_mlp_noalloc")
@@ -325,6 +506,8 @@ class Dispatcher:
         F, wdtype = self._check_w1(w1, w1_scales)
         self._check_perm(perm, perm_scales)
         self._check_scratch(scratch, F, wdtype)
+        if wdtype == "int4":
+            _check_current_device(perm=perm)
         A.check(A.lib().moe_grouped_fc1_swiglu(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(scratch), scratch.numel(), _stream()),
                 "moe_grouped_fc1_swiglu")
@@ -344,6 +527,8 @@ class Dispatcher:
         self._check_scratch(scratch, F, wdtype)
         self._check_after_fc1(F, wdtype, scratch)
         self._check_expert_out(out)
+        if wdtype == "int4":
+            _check_current_device(out=out)
         A.check(A.lib().moe_grouped_fc2(C.byref(self.h), F, _DT[wdtype], _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                         scratch.numel(), _ptr(out), _stream()), "moe_grouped_fc2")
         return out
@@ -519,14 +704,26 @@ class Dispatcher:
         return out
 
     def layer(self, x, routing, probs, w1, w2, *, perm=None, perm_scales=None, scratch=None, expert_out=None,
-              out=None, w1_scales=None, w2_scales=None, T_live=None, apply_probs=True, check_overflow=False):
-        """dispatch -> grouped MLP -> combine on the current stream.  With a
+              out=None, w1_scales=None, w2_scales=None, T_live=None, apply_probs=True, check_overflow=False,
+              norm=None, router=None, gate=None):
+        """dispatch -> grouped MLP -> combine on the current stream.  With
+        ``norm`` = (weight, bias) or (weight, bias, eps), the layer reads
+        layer_norm(x) in bf16 in place of x.  With ``router``, a callable that takes the
+        rows the layer reads and returns their logits [T,E], routing and probs
+        (None then) are ``self.gate`` of those logits, with the keyword
+        arguments ``gate`` (bias, score, normalize, scale).  With a
         handle of fp8 payload and bf16 tokens, dispatch quantises on the way
         (routing metadata, then moe_permute_quantize into e4m3 rows ``perm``
         with 1x128 scales ``perm_scales``).  With ``check_overflow``, a
         device-side assert on the overflow flag is enqueued after the combine
         (no host wait; capturable).  Buffers the caller omits are allocated
         per call."""
+        _need(router is not None or gate is None, "gate needs a router")
+        if norm is not None:
+            x, _, _ = layer_norm(x, *norm, out_dtype=torch.bfloat16)
+        if router is not None:
+            _need(routing is None and probs is None, "routing and probs come from the router's logits")
+            routing, probs = self.gate(router(x), **(gate or {}))
         if self.payload == A.FP8E4M3_B128 and x.dtype == torch.bfloat16:
             _, flag = self.preprocess(routing, probs, T_live)
             perm, perm_scales = self.permute_quantize(x, out=perm, out_scales=perm_scales)

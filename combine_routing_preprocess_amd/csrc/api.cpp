@@ -243,6 +243,7 @@ size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype) {
     if (!h || F <= 0) return 0;
     const size_t R = (size_t)h->desc.out_rows;
     if (wdtype == MOE_BF16) return up(R * (size_t)F * 2, kAlign);
+    if (wdtype == MOE_INT4_G128) return F % 128 || h->desc.H % 128 ? 0 : up(R * (size_t)F * 2, kAlign);
     if (wdtype == MOE_FP8E4M3_B128) {
         if (F % 128 || h->desc.H % 128) return 0;
         return up(fp8_mlp_scratch_bytes((long long)R, h->desc.H, F), kAlign);
@@ -265,7 +266,7 @@ int check_mlp_weights(const moe_handle* h, int32_t F, int32_t wdtype, const void
     if (wdtype == MOE_BF16) {
         if (w_scales) return MOE_EDTYPE;
         if (d.H % 256 || F % 128) return MOE_ESHAPE;
-    } else if (wdtype == MOE_FP8E4M3_B128) {
+    } else if (wdtype == MOE_FP8E4M3_B128 || wdtype == MOE_INT4_G128) {
         if (!w_scales) return MOE_EINVAL;
         if (!al4(w_scales)) return MOE_EALIGN;
         if (d.H % 128 || F % 128) return MOE_ESHAPE;
@@ -331,6 +332,8 @@ int moe_grouped_fc1_swiglu(const moe_handle* h, int32_t F, int32_t wdtype, const
     if (wdtype == MOE_FP8E4M3_B128)
         return hip_rc(launch_gemm_fp8(h, 0, F, d_perm, d_perm_scales, d_w1, d_w1_scales, d_scratch, nullptr,
                                       (hipStream_t)stream));
+    if (wdtype == MOE_INT4_G128)
+        return hip_rc(launch_gemm_int4(h, 0, F, d_perm, d_w1, d_w1_scales, d_scratch, (hipStream_t)stream));
     return hip_rc(launch_gemm_bf16(h, 0, F, d_perm, d_w1, d_scratch, nullptr, ncu, (hipStream_t)stream));
 }
 
@@ -345,6 +348,8 @@ int moe_grouped_fc2(const moe_handle* h, int32_t F, int32_t wdtype, const void* 
     if (wdtype == MOE_FP8E4M3_B128)
         return hip_rc(launch_gemm_fp8(h, 1, F, nullptr, nullptr, d_w2, d_w2_scales, d_scratch, d_expert_out,
                                       (hipStream_t)stream));
+    if (wdtype == MOE_INT4_G128)
+        return hip_rc(launch_gemm_int4(h, 1, F, d_scratch, d_w2, d_w2_scales, d_expert_out, (hipStream_t)stream));
     return hip_rc(launch_gemm_bf16(h, 1, F, d_scratch, d_w2, d_expert_out, nullptr, ncu, (hipStream_t)stream));
 }
 
@@ -490,6 +495,98 @@ int moe_combine_backward(const moe_handle* h, const void* d_grad_y, const void* 
     if (d.H % 8) return MOE_ESHAPE;
     return hip_rc(launch_combine_backward(h, d_grad_y, d_expert_out, apply_probs ? 1 : 0, d_grad_expert_out,
                                           d_grad_probs, (hipStream_t)stream));
+}
+
+namespace {
+
+bool row_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_F32; }
+
+// Checks shared by the gate and its backward pass: score, type and the three
+// arrays in the shapes of logits and routing.
+int check_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, int32_t score, float scale,
+               const void* d_routing, const float* d_probs) {
+    int rc = check_handle(h, false);
+    if (rc) return rc;
+    if (!row_dtype(logit_dtype)) return MOE_EDTYPE;
+    if ((score != MOE_GATE_SOFTMAX && score != MOE_GATE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
+    if (h->desc.T > 0 && (!d_logits || !d_routing || !d_probs)) return MOE_EINVAL;
+    if (!al16(d_logits) || !al16(d_routing) || !al4(d_probs)) return MOE_EALIGN;
+    return MOE_OK;
+}
+
+// Checks shared by the layer norm and its backward pass.
+int check_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w_dtype) {
+    if (T < 0 || H < 1 || H > MOE_NORM_MAX_H) return MOE_ESHAPE;
+    return row_dtype(x_dtype) && row_dtype(y_dtype) && row_dtype(w_dtype) ? MOE_OK : MOE_EDTYPE;
+}
+
+size_t row_bytes(int32_t T, int32_t H, int32_t dtype) { return (size_t)T * H * (dtype == MOE_BF16 ? 2 : 4); }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return p < q + nb && q < p + na;
+}
+
+}  // namespace
+
+int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, const float* d_bias, int32_t score,
+             int32_t normalize, float scale, void* d_routing, float* d_probs, void* stream) {
+    int rc = check_gate(h, d_logits, logit_dtype, score, scale, d_routing, d_probs);
+    if (rc) return rc;
+    if (d_bias && !al4(d_bias)) return MOE_EALIGN;
+    return hip_rc(launch_gate(h, d_logits, logit_dtype, d_bias, score == MOE_GATE_SIGMOID, normalize ? 1 : 0, scale,
+                              d_routing, d_probs, (hipStream_t)stream));
+}
+
+int moe_gate_backward(const moe_handle* h, const float* d_grad_probs, const void* d_logits, int32_t logit_dtype,
+                      const void* d_routing, int32_t score, int32_t normalize, float scale, void* d_grad_logits,
+                      void* stream) {
+    int rc = check_gate(h, d_logits, logit_dtype, score, scale, d_routing, d_grad_probs);
+    if (rc) return rc;
+    if (h->desc.T > 0 && !d_grad_logits) return MOE_EINVAL;
+    if (!al16(d_grad_logits)) return MOE_EALIGN;
+    return hip_rc(launch_gate_backward(h, d_grad_probs, d_logits, logit_dtype, d_routing, score == MOE_GATE_SIGMOID,
+                                       normalize ? 1 : 0, scale, d_grad_logits, (hipStream_t)stream));
+}
+
+int moe_layer_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w_dtype, const void* d_x,
+                   const void* d_weight, const void* d_bias, float eps, void* d_y, float* d_mean, float* d_rstd,
+                   void* stream) {
+    int rc = check_norm(T, H, x_dtype, y_dtype, w_dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return MOE_EINVAL;
+    if (T > 0 && (!d_x || !d_y)) return MOE_EINVAL;
+    if (!al16(d_x) || !al16(d_y) || !al16(d_weight) || !al16(d_bias) || !al4(d_mean) || !al4(d_rstd))
+        return MOE_EALIGN;
+    if (overlap(d_x, row_bytes(T, H, x_dtype), d_y, row_bytes(T, H, y_dtype))) return MOE_EINVAL;
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
+    return hip_rc(launch_layer_norm(T, H, x_dtype, y_dtype, w_dtype, d_x, d_weight, d_bias, eps, d_y, d_mean, d_rstd,
+                                    ncu, (hipStream_t)stream));
+}
+
+size_t moe_layer_norm_backward_scratch_bytes(int32_t T, int32_t H) {
+    if (check_norm(T, H, MOE_F32, MOE_F32, MOE_F32)) return 0;
+    return up(norm_backward_scratch_bytes(T, H) + 1, kAlign);
+}
+
+int moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w_dtype,
+                            const void* d_grad_y, const void* d_x, const float* d_mean, const float* d_rstd,
+                            const void* d_weight, void* d_grad_x, float* d_grad_weight, float* d_grad_bias,
+                            void* d_scratch, size_t scratch_bytes, void* stream) {
+    int rc = check_norm(T, H, x_dtype, y_dtype, w_dtype);
+    if (rc) return rc;
+    if (T > 0 && (!d_grad_y || !d_x || !d_mean || !d_rstd || !d_grad_x)) return MOE_EINVAL;
+    const bool params = d_grad_weight || d_grad_bias;
+    if (params && !d_scratch) return MOE_EINVAL;
+    if (!al16(d_grad_y) || !al16(d_x) || !al4(d_mean) || !al4(d_rstd) || !al16(d_weight) || !al16(d_grad_x) ||
+        !al16(d_grad_weight) || !al16(d_grad_bias) || !al16(d_scratch))
+        return MOE_EALIGN;
+    if (params && scratch_bytes < moe_layer_norm_backward_scratch_bytes(T, H)) return MOE_ENOSPC;
+    const size_t nx = row_bytes(T, H, x_dtype);
+    if (overlap(d_grad_x, nx, d_x, nx) || overlap(d_grad_x, nx, d_grad_y, row_bytes(T, H, y_dtype))) return MOE_EINVAL;
+    return hip_rc(launch_layer_norm_backward(T, H, x_dtype, y_dtype, w_dtype, d_grad_y, d_x, d_mean, d_rstd, d_weight,
+                                             d_grad_x, d_grad_weight, d_grad_bias, d_scratch, (hipStream_t)stream));
 }
 
 }  // extern "C"

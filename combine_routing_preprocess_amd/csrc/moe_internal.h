@@ -100,6 +100,24 @@ hipError_t launch_gemm_bf16(const moe_handle* h, int stage, int F, const void* i
 hipError_t launch_gemm_fp8(const moe_handle* h, int stage, int F, const void* in, const float* in_scales,
                            const void* w, const float* ws, void* scratch, void* out, hipStream_t s);
 size_t fp8_mlp_scratch_bytes(long long R, int H, int F);
+// 4-bit weights: stage 0 FC1 + SwiGLU (bf16 rows -> bf16 activations), stage
+// 1 FC2 (bf16 activations -> bf16 expert output); rows without a copy are
+// not written
+hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* in, const void* w, const float* ws,
+                            void* out, hipStream_t s);
+// layer norm of rows and its backward pass; the gate and its backward pass
+size_t norm_backward_scratch_bytes(int T, int H);
+hipError_t launch_layer_norm(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x, const void* weight,
+                             const void* bias, float eps, void* y, float* mean, float* rstd, int num_cu,
+                             hipStream_t s);
+hipError_t launch_layer_norm_backward(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* gy,
+                                      const void* x, const float* mean, const float* rstd, const void* weight,
+                                      void* gx, float* gw, float* gb, void* scratch, hipStream_t s);
+hipError_t launch_gate(const moe_handle* h, const void* logits, int logit_dtype, const float* bias, int sigmoid,
+                       int normalize, float scale, void* routing, float* probs, hipStream_t s);
+hipError_t launch_gate_backward(const moe_handle* h, const float* grad_probs, const void* logits, int logit_dtype,
+                                const void* routing, int sigmoid, int normalize, float scale, void* grad_logits,
+                                hipStream_t s);
 // persistent decode layer (quantise-on-dispatch, FC1, activation quantiser,
 // FC2, combine in one launch after a control-block reset)
 size_t decode_layer_scratch_bytes(long long R, int H, int F);

@@ -67,11 +67,15 @@ enum moe_route_fmt {
     MOE_ROUTE_SPARSE_BOOL = 2
 };
 
-/* ---- payload / weight dtypes ([P2] "Full HybridEP reference validation":
+/* ---- payload / weight / row dtypes ([P2] "Full HybridEP reference validation":
  * BF16 and FP8 dispatch; [P5] first commit message: low-precision weights) */
 enum moe_dtype {
     MOE_BF16 = 0,
-    MOE_FP8E4M3_B128 = 1    /* e4m3 codes + fp32 scale per 128 columns         */
+    MOE_FP8E4M3_B128 = 1,   /* e4m3 codes + fp32 scale per 128 columns         */
+    MOE_F32 = 2,            /* rows and parameters of the layer norm, logits   */
+    MOE_INT4_G128 = 3       /* expert weights: two 4-bit codes per byte (even  */
+                            /* column in the low half), value (code - 8) times */
+                            /* one fp32 scale per weight row and 128 columns   */
 };
 
 /* ---- overflow flag bits ([P3] "What does this PR do ?", "Validation": the
@@ -219,7 +223,8 @@ int moe_dispatch(moe_handle* h, const void* d_routing, const float* d_probs,
  * activations of all R rows;
  * MOE_FP8E4M3_B128 holds the fp32 FC1 activations plus the e4m3 codes and
  * fp32 1x128 scales of the permuted rows and of the activations (each input
- * is quantised once per call).  0 if invalid. */
+ * is quantised once per call); MOE_INT4_G128 holds bf16 activations.  0 if
+ * invalid. */
 size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype);
 
 /* Grouped expert MLP over the permuted rows: for every expert e and every
@@ -242,6 +247,12 @@ size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype);
  *          nearest-even, saturating) and a is re-quantised the same way
  *          before FC2; requires H, F multiples of 128.  Built for decode-sized
  *          batches (few rows per expert; weight streaming bound).
+ *   wdtype MOE_INT4_G128: d_w1 [E,2F,H/2] codes, d_w1_scales [E,2F,H/128]
+ *          fp32, d_w2 [E,H,F/2] codes, d_w2_scales [E,H,F/128] fp32; the rows
+ *          stay bf16 (bf16 payload only), products and scales are fp32, a is
+ *          rounded once to bf16 before FC2 as with bf16 weights; requires H,
+ *          F multiples of 128.  Rows that hold no kept copy are not written.
+ *          Built for decode-sized batches, as fp8.
  *   d_scratch     >= moe_mlp_scratch_bytes bytes
  *   d_expert_out  [R,H] bf16; rows that hold no kept copy are unspecified */
 int moe_grouped_swiglu_mlp(const moe_handle* h, int32_t F, int32_t wdtype, const void* d_perm,
@@ -428,6 +439,83 @@ int moe_dispatch_backward(const moe_handle* h, const void* d_grad_out, const flo
  *   d_grad_probs      nullable out, the routing's shape */
 int moe_combine_backward(const moe_handle* h, const void* d_grad_y, const void* d_expert_out,
                          int32_t apply_probs, void* d_grad_expert_out, float* d_grad_probs, void* stream);
+
+/* ---- gate (expert choice from router logits, and its gradient) --------------
+ * The step before moe_route_preprocess: the K experts of each token and their
+ * weights, written in the handle's routing format (desc.route_fmt) as the
+ * d_routing and d_probs that moe_route_preprocess takes.  [P4] "Motivation"
+ * (the dispatcher takes the router's top-k indices and weights), [P2]
+ * "Implementation" (Boolean map or dense indices).  Needs no routing metadata
+ * on the handle and leaves the handle as it is.
+ *   score   s_e = softmax over the row (MOE_GATE_SOFTMAX) or sigmoid
+ *           (MOE_GATE_SIGMOID) of the logits
+ *   choice  the K experts of the largest key: the logit, or with d_bias the
+ *           score + bias (in 64 bits); equal keys go to the lowest expert.  An
+ *           expert whose logit or key is NaN or -inf is never chosen and has
+ *           no share of the softmax: -inf logits switch experts off.  Dense
+ *           slots are in order of falling key; slots left over are -1 with
+ *           weight 0 (a row without candidates is unrouted)
+ *   weight  scale * s_j, or with `normalize` scale * s_j / sum of the chosen s
+ * A +inf logit is chosen first; its row's softmax weights are NaN, and with a
+ * bias its row's softmax keys are, so that the row is unrouted.
+ *   logit_dtype  MOE_BF16 or MOE_F32 (else MOE_EDTYPE)
+ *   d_logits     [T,E]
+ *   d_bias       nullable [E] fp32; steers the choice only
+ *   d_routing    out, [T,K] int16 / int32 or [T,E] uint8 (0 / 1)
+ *   d_probs      out, fp32 in the routing's shape; 0 where nothing is chosen */
+enum moe_gate_score { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
+int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, const float* d_bias, int32_t score,
+             int32_t normalize, float scale, void* d_routing, float* d_probs, void* stream);
+
+/* Backward of the gate: the gradient of the weights (as moe_combine_backward
+ * or moe_dispatch_backward give it, in the routing's shape) to the logits,
+ * with the choice held fixed (the bias has no gradient).  Entries of empty
+ * slots (an index outside [0, E)), of unrouted experts and of experts whose
+ * logit is NaN or -inf are ignored; a repeated index counts once per slot.
+ * Every element of d_grad_logits is written.
+ *   d_grad_probs   fp32 in the routing's shape
+ *   d_logits       [T,E] the forward's logits
+ *   d_routing      the forward's routing
+ *   d_grad_logits  [T,E] out, of logit_dtype */
+int moe_gate_backward(const moe_handle* h, const float* d_grad_probs, const void* d_logits, int32_t logit_dtype,
+                      const void* d_routing, int32_t score, int32_t normalize, float scale, void* d_grad_logits,
+                      void* stream);
+
+/* ---- layer norm (rows in front of the layer, and its gradients) -------------
+ * y = (x - mu) * rstd * weight + bias per row, mu = mean of the row, rstd =
+ * 1 / sqrt(mean((x - mu)^2) + eps); statistics in fp32, one rounding to the
+ * output's type.  The rows are those that the router and the dispatch read.
+ * No handle: T rows of H elements, contiguous, 1 <= H <= MOE_NORM_MAX_H; rows
+ * need no alignment beyond d_x's own 16 bytes.
+ *   x_dtype, y_dtype, w_dtype  MOE_BF16 or MOE_F32 each (else MOE_EDTYPE)
+ *   d_x            [T,H]
+ *   d_weight, d_bias  nullable [H] of w_dtype (1 and 0 where absent)
+ *   eps            >= 0 and finite (else MOE_EINVAL)
+ *   d_y            [T,H] out; must not overlap d_x
+ *   d_mean, d_rstd nullable [T] fp32 out: what the backward pass needs */
+#define MOE_NORM_MAX_H 32768
+int moe_layer_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w_dtype, const void* d_x,
+                   const void* d_weight, const void* d_bias, float eps, void* d_y, float* d_mean, float* d_rstd,
+                   void* stream);
+
+/* Backward of the layer norm.  With xh = (x - mean) * rstd and g = grad_y *
+ * weight: grad_x = rstd * (g - mean(g) - xh * mean(g * xh)) per row,
+ * grad_weight = sum over the rows of grad_y * xh, grad_bias = sum over the
+ * rows of grad_y, both fp32, added in a fixed order (a call repeats bit for
+ * bit) and written fresh (zeros when T = 0).
+ *   d_grad_y       [T,H] of y_dtype
+ *   d_x, d_mean, d_rstd  the forward's input and outputs
+ *   d_weight       nullable [H] of w_dtype
+ *   d_grad_x       [T,H] out, of x_dtype; must not overlap d_x or d_grad_y
+ *   d_grad_weight, d_grad_bias  nullable [H] fp32 out
+ *   d_scratch      >= moe_layer_norm_backward_scratch_bytes(T, H) bytes
+ *                  (MOE_ENOSPC if smaller); two calls that share it must not
+ *                  overlap.  May be NULL with both parameter gradients NULL. */
+size_t moe_layer_norm_backward_scratch_bytes(int32_t T, int32_t H);
+int moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w_dtype,
+                            const void* d_grad_y, const void* d_x, const float* d_mean, const float* d_rstd,
+                            const void* d_weight, void* d_grad_x, float* d_grad_weight, float* d_grad_bias,
+                            void* d_scratch, size_t scratch_bytes, void* stream);
 
 /* ---- caller-owned buffer ring ------------------------------------------------
  * [P1] "Summary", "Motivation", "Known limitations": dispatch outputs and FC2
