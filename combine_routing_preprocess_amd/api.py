@@ -19,17 +19,19 @@ _FMT_DTYPES = {A.ROUTE_DENSE_I16: (torch.int16,), A.ROUTE_DENSE_I32: (torch.int3
                A.ROUTE_SPARSE_BOOL: (torch.uint8, torch.bool, torch.int8)}
 _DT = {"bf16": A.BF16, "fp8": A.FP8E4M3_B128, "int4": A.INT4_G128}
 _ROW_DT = {torch.bfloat16: A.BF16, torch.float32: A.F32}
+_F32 = (torch.float32,)
 _SCORE = {"softmax": A.GATE_SOFTMAX, "sigmoid": A.GATE_SIGMOID}
 _ROUTING_OUT = {A.ROUTE_DENSE_I16: torch.int16, A.ROUTE_DENSE_I32: torch.int32, A.ROUTE_SPARSE_BOOL: torch.uint8}
 _FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()      # c_void_p arguments take addresses as they are
 
 
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle, without building a Stream object (2.9 us of a call that launches in 4)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _need(cond: bool, msg: str):
@@ -65,27 +67,32 @@ def assert_no_overflow(flag: torch.Tensor) -> None:
     torch._assert_async(flag[0] == 0)
 
 
+# The checks below run on every call of a few microseconds: messages are only
+# put together where a check fails.
 def _check_rows(t, name, shape, dtypes):
-    _need(t.dtype in dtypes and tuple(t.shape) == shape, f"{name} must be {' or '.join(str(d) for d in dtypes)} "
-          f"{list(shape)}, got {t.dtype} {list(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if t.dtype not in dtypes or t.shape != shape:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _check_current_device(**tensors):
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else None
     for name, t in tensors.items():
-        _need(t is None or (t.is_cuda and t.device.index == torch.cuda.current_device()),
-              f"{name} must live on the current GPU")
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"{name} must live on the current GPU")
 
 
 def _check_norm_params(H, **params):
     """The parameters' common dtype (float32 where there are none)."""
-    kinds = set()
+    kind = None
     for name, p in params.items():
         if p is not None:
-            _check_rows(p, name, (H,), tuple(_ROW_DT))
-            kinds.add(p.dtype)
-    _need(len(kinds) <= 1, "weight and bias must share their dtype")
-    return _ROW_DT[kinds.pop()] if kinds else A.F32
+            _check_rows(p, name, (H,), _ROW_DT)
+            _need(kind is None or p.dtype == kind, "weight and bias must share their dtype")
+            kind = p.dtype
+    return A.F32 if kind is None else _ROW_DT[kind]
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -96,18 +103,18 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     layer_norm_backward.  ``out`` is of ``out_dtype`` (default: x's)."""
     _need(x.dim() == 2, "x must be [T,H]")
     T, H = x.shape
-    _check_rows(x, "x", (T, H), tuple(_ROW_DT))
+    _check_rows(x, "x", (T, H), _ROW_DT)
     wdt = _check_norm_params(H, weight=weight, bias=bias)
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=x.device)
-    _check_rows(out, "out", (T, H), tuple(_ROW_DT) if out_dtype is None else (out_dtype,))
+    _check_rows(out, "out", (T, H), _ROW_DT)
+    _need(out_dtype is None or out.dtype == out_dtype, "out must be of out_dtype")
     if mean is None:
         mean = torch.empty(T, dtype=torch.float32, device=x.device)
     if rstd is None:
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    _check_rows(mean, "mean", (T,), (torch.float32,))
-    _check_rows(rstd, "rstd", (T,), (torch.float32,))
-    _need(out.dtype in _ROW_DT, f"out must be bfloat16 or float32, got {out.dtype}")
+    _check_rows(mean, "mean", (T,), _F32)
+    _check_rows(rstd, "rstd", (T,), _F32)
     _check_current_device(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
     A.check(A.lib().moe_layer_norm(T, H, _ROW_DT[x.dtype], _ROW_DT[out.dtype], wdt, _ptr(x), _ptr(weight), _ptr(bias),
                                    float(eps), _ptr(out), _ptr(mean), _ptr(rstd), _stream()), "moe_layer_norm")
@@ -127,10 +134,10 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
     mean and rstd are the forward's."""
     _need(x.dim() == 2, "x must be [T,H]")
     T, H = x.shape
-    _check_rows(x, "x", (T, H), tuple(_ROW_DT))
-    _check_rows(grad_y, "grad_y", (T, H), tuple(_ROW_DT))
-    _check_rows(mean, "mean", (T,), (torch.float32,))
-    _check_rows(rstd, "rstd", (T,), (torch.float32,))
+    _check_rows(x, "x", (T, H), _ROW_DT)
+    _check_rows(grad_y, "grad_y", (T, H), _ROW_DT)
+    _check_rows(mean, "mean", (T,), _F32)
+    _check_rows(rstd, "rstd", (T,), _F32)
     wdt = _check_norm_params(H, weight=weight)
     if out is None:
         out = torch.empty_like(x)
@@ -140,14 +147,16 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
             grad_weight = torch.empty(H, dtype=torch.float32, device=x.device)
         if grad_bias is None:
             grad_bias = torch.empty(H, dtype=torch.float32, device=x.device)
-        _check_rows(grad_weight, "grad_weight", (H,), (torch.float32,))
-        _check_rows(grad_bias, "grad_bias", (H,), (torch.float32,))
+        _check_rows(grad_weight, "grad_weight", (H,), _F32)
+        _check_rows(grad_bias, "grad_bias", (H,), _F32)
         need = layer_norm_backward_scratch_bytes(T, H)
-        _need(need > 0, f"rows of {H} elements are outside 1..{A.NORM_MAX_H}")
+        if need == 0:
+            raise ValueError(f"rows of {H} elements are outside 1..{A.NORM_MAX_H}")
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=x.device)
         _need(scratch.is_contiguous(), "scratch must be contiguous")
-        _need(scratch.numel() * scratch.element_size() >= need, f"scratch holds fewer than the {need} bytes needed")
+        if scratch.numel() * scratch.element_size() < need:
+            raise ValueError(f"scratch holds fewer than the {need} bytes needed")
     else:
         _need(grad_weight is None and grad_bias is None, "grad_weight and grad_bias need want_params")
     _check_current_device(grad_y=grad_y, x=x, mean=mean, rstd=rstd, weight=weight, out=out, grad_weight=grad_weight,
@@ -214,16 +223,19 @@ class Dispatcher:
 
     # ---- checks ------------------------------------------------------------------
     def _dev(self, t: torch.Tensor, name: str):
-        _need(t.device == self.device or (t.device.type == "cuda" and self.device.type == "cuda"
-                                          and t.device.index == torch.cuda.current_device()),
-              f"{name} must live on {self.device}")
-        _need(t.is_contiguous(), f"{name} must be contiguous")
+        if not (t.device == self.device or (t.device.type == "cuda" and self.device.type == "cuda"
+                                            and t.device.index == torch.cuda.current_device())):
+            raise ValueError(f"{name} must live on {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
     def _check_routing(self, routing, probs, T_live):
         self._dev(routing, "routing")
-        _need(routing.dtype in _FMT_DTYPES[self.route_fmt], f"routing dtype {routing.dtype} does not match the format")
-        shape = (self.T, self.E) if self.route_fmt == A.ROUTE_SPARSE_BOOL else (self.T, self.K)
-        _need(tuple(routing.shape) == shape, f"routing shape {tuple(routing.shape)} != {shape}")
+        if routing.dtype not in _FMT_DTYPES[self.route_fmt]:
+            raise ValueError(f"routing dtype {routing.dtype} does not match the format")
+        shape = self._routing_shape()
+        if routing.shape != shape:
+            raise ValueError(f"routing shape {tuple(routing.shape)} != {shape}")
         if probs is not None:
             self._dev(probs, "probs")
             _need(probs.dtype == torch.float32 and tuple(probs.shape) == shape, "probs must be float32 shaped like routing")
@@ -237,9 +249,9 @@ class Dispatcher:
 
     def _check_gate(self, logits, score):
         self._dev(logits, "logits")
-        _need(logits.dtype in _ROW_DT and tuple(logits.shape) == (self.T, self.E),
-              f"logits must be bfloat16 or float32 [{self.T}, {self.E}], got {logits.dtype} {tuple(logits.shape)}")
-        _need(score in _SCORE, f"score must be one of {sorted(_SCORE)}, got {score!r}")
+        _check_rows(logits, "logits", (self.T, self.E), _ROW_DT)
+        if score not in _SCORE:
+            raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
 
     def gate(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, *, score: str = "softmax",
              normalize: bool = False, scale: float = 1.0, routing: Optional[torch.Tensor] = None,
@@ -389,8 +401,9 @@ class Dispatcher:
         [E, 2F, H/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w1, "w1")
         if self._is_int4(w1, w1_scales):
-            _need(w1.shape[0] == self.E and 2 * w1.shape[2] == self.H and w1.shape[1] % 2 == 0 and w1.shape[1] > 0,
-                  f"4-bit w1 must be [E, 2F, H/2] = [{self.E}, 2F, {self.H // 2}], got {tuple(w1.shape)}")
+            if not (w1.shape[0] == self.E and 2 * w1.shape[2] == self.H and w1.shape[1] % 2 == 0 and w1.shape[1] > 0):
+                raise ValueError(f"4-bit w1 must be [E, 2F, H/2] = [{self.E}, 2F, {self.H // 2}], "
+                                 f"got {tuple(w1.shape)}")
             return int(w1.shape[1]) // 2, self._check_int4(w1, w1_scales, "w1")
         _need(w1.dim() == 3 and w1.shape[0] == self.E and w1.shape[2] == self.H and w1.shape[1] % 2 == 0
               and w1.shape[1] > 0, f"w1 must be [E, 2F, H] = [{self.E}, 2F, {self.H}], got {tuple(w1.shape)}")
@@ -403,8 +416,8 @@ class Dispatcher:
         [E, H, F/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w2, "w2")
         if self._is_int4(w2, w2_scales):
-            _need(w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0,
-                  f"4-bit w2 must be [E, H, F/2] = [{self.E}, {self.H}, F/2], got {tuple(w2.shape)}")
+            if not (w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0):
+                raise ValueError(f"4-bit w2 must be [E, H, F/2] = [{self.E}, {self.H}, F/2], got {tuple(w2.shape)}")
             return 2 * int(w2.shape[2]), self._check_int4(w2, w2_scales, "w2")
         _need(w2.dim() == 3 and w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0,
               f"w2 must be [E, H, F] = [{self.E}, {self.H}, F], got {tuple(w2.shape)}")
@@ -420,12 +433,12 @@ class Dispatcher:
 
     def _check_int4(self, w, scales, name) -> str:
         cols = 2 * int(w.shape[2])
-        _need(self.H % 128 == 0 and w.shape[1] % 128 == 0 and cols % 128 == 0,
-              f"4-bit {name} needs dimensions that are multiples of 128")
+        if self.H % 128 or w.shape[1] % 128 or cols % 128:
+            raise ValueError(f"4-bit {name} needs dimensions that are multiples of 128")
         shape = (self.E, int(w.shape[1]), cols // 128)
-        self._dev(scales, f"{name}_scales")
-        _need(scales.dtype == torch.float32 and tuple(scales.shape) == shape,
-              f"{name}_scales must be float32 {shape}, got {scales.dtype} {tuple(scales.shape)}")
+        self._dev(scales, name + "_scales")
+        if scales.dtype != torch.float32 or scales.shape != shape:
+            raise ValueError(f"{name}_scales must be float32 {shape}, got {scales.dtype} {tuple(scales.shape)}")
         return "int4"
 
     def _check_wdtype(self, w, scales, name, scale_shape):
@@ -444,13 +457,15 @@ class Dispatcher:
     def _check_scratch(self, scratch: torch.Tensor, F: int, wdtype: str):
         self._dev(scratch, "scratch")
         need = self.mlp_scratch_bytes(F, wdtype)
-        _need(need > 0, f"invalid FFN width {F} for {wdtype} weights")
-        _need(scratch.numel() * scratch.element_size() >= need, f"scratch holds fewer than the {need} bytes needed")
+        if need <= 0:
+            raise ValueError(f"invalid FFN width {F} for {wdtype} weights")
+        if scratch.numel() * scratch.element_size() < need:
+            raise ValueError(f"scratch holds fewer than the {need} bytes needed")
 
     def _check_expert_out(self, out: torch.Tensor):
         self._dev(out, "out")
-        _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (self.R, self.H),
-              f"out must be bf16 [R, H] = [{self.R}, {self.H}]")
+        if out.dtype != torch.bfloat16 or out.shape != (self.R, self.H):
+            raise ValueError(f"out must be bf16 [R, H] = [{self.R}, {self.H}]")
 
     def grouped_mlp(self, perm: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, *,
                     w1_scales: Optional[torch.Tensor] = None, w2_scales: Optional[torch.Tensor] = None,

@@ -25,10 +25,14 @@
 // as 16-byte accesses at element alignment, which the memory pipeline takes
 // (the whole-line rows of a width that is a multiple of 8 are just the fast
 // case), and a last partial chunk goes element by element.
-#include "moe_internal.h"
+#include "wave_ops.h"
 
 namespace moe {
 namespace {
+
+using ops::readlane;
+using ops::row_sum;
+using ops::wave_sum_dpp;
 
 typedef u32x4 u32x4_e __attribute__((aligned(2)));   // 16 bytes at element alignment
 
@@ -38,13 +42,15 @@ struct Chunk {
     u32x4 w[sizeof(XT) / 2];
 };
 
-// Elements 0 .. n-1 of a chunk (n <= 8; the rest reads as zero).
-template <typename XT>
+// Elements 0 .. n-1 of a chunk (n <= 8; the rest reads as zero).  TAIL: n may
+// lie between 0 and 8 (rows whose length is no multiple of 8).
+template <bool TAIL, typename XT>
 __device__ __forceinline__ Chunk<XT> load_chunk(const XT* p, int n) {
     Chunk<XT> c;
-    if (n >= 8) {
+    if (!TAIL || n >= 8) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(XT) / 2); ++i) c.w[i] = ((const u32x4_e*)p)[i];
+        for (int i = 0; i < (int)(sizeof(XT) / 2); ++i)
+            c.w[i] = TAIL || n >= 8 ? ((const u32x4_e*)p)[i] : u32x4{0u, 0u, 0u, 0u};
         return c;
     }
     if constexpr (sizeof(XT) == 2) {
@@ -69,20 +75,28 @@ __device__ __forceinline__ void unpack(const Chunk<XT>& c, float (&v)[8]) {
     }
 }
 
-template <typename XT>
+// STREAM: nontemporal stores.
+template <bool TAIL, bool STREAM = false, typename XT>
 __device__ __forceinline__ void store_chunk(XT* p, int n, const float (&v)[8]) {
     if (n >= 8) {
+        u32x4 w[sizeof(XT) / 2];
         if constexpr (sizeof(XT) == 2) {
-            *(u32x4_e*)p = u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
-                                 bf16x2_rne(v[6], v[7])};
+            w[0] = u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                         bf16x2_rne(v[6], v[7])};
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                ((u32x4_e*)p)[i] = u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+                w[i] = u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                             __float_as_uint(v[4 * i + 3])};
+        }
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(XT) / 2); ++i) {
+            if constexpr (STREAM) __builtin_nontemporal_store(w[i], (u32x4_e*)p + i);
+            else ((u32x4_e*)p)[i] = w[i];
         }
         return;
     }
+    if constexpr (!TAIL) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < n) {
@@ -92,21 +106,16 @@ __device__ __forceinline__ void store_chunk(XT* p, int n, const float (&v)[8]) {
 }
 
 // Chunk of a weight or bias vector; `fill` where there is none.
+template <bool TAIL>
 __device__ __forceinline__ void load_param(const void* p, int dtype, int c, int n, float fill, float (&v)[8]) {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = fill;
     } else if (dtype == MOE_BF16) {
-        unpack(load_chunk((const uint16_t*)p + 8 * c, n), v);
+        unpack(load_chunk<TAIL>((const uint16_t*)p + 8 * c, n), v);
     } else {
-        unpack(load_chunk((const float*)p + 8 * c, n), v);
+        unpack(load_chunk<TAIL>((const float*)p + 8 * c, n), v);
     }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
 }
 
 constexpr int kMaxWaves = 16;   // wavefronts of a workgroup
@@ -120,41 +129,51 @@ __device__ __forceinline__ int part_elems(int H, int W, int i) {
     return n;
 }
 
-template <typename XT, typename YT, int NC>
+template <typename XT, typename YT, int NC, bool TAIL, bool STREAM>
 __global__ __launch_bounds__(1024) void k_layer_norm(const XT* __restrict__ x, int T, int H, int W, int G,
                                                      const void* __restrict__ weight, const void* __restrict__ bias,
                                                      int wdtype, float eps, YT* __restrict__ y,
                                                      float* __restrict__ mean, float* __restrict__ rstd) {
-    __shared__ float s_m[2][kMaxWaves], s_e[2][kMaxWaves], s_q[2][kMaxWaves];
+    __shared__ float4 s_part[2][kMaxWaves];   // each part's m, e, q
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int grp = wave / W, part = wave - grp * W;
+    constexpr bool KEEP = NC <= 2;   // parameters and the next row in registers
     int col[NC], n[NC];
-    float w[NC][8], b[NC][8];
+    float w[KEEP ? NC : 1][8], b[KEEP ? NC : 1][8];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
         const int c = (part + k * W) * 64 + lane;
         col[k] = 8 * c;
         n[k] = min(max(H - col[k], 0), 8);
-        load_param(weight, wdtype, c, n[k], 1.f, w[k]);
-        load_param(bias, wdtype, c, n[k], 0.f, b[k]);
+        if (KEEP) {
+            load_param<TAIL>(weight, wdtype, c, n[k], 1.f, w[KEEP ? k : 0]);
+            load_param<TAIL>(bias, wdtype, c, n[k], 0.f, b[KEEP ? k : 0]);
+        }
     }
     const float inv_h = 1.f / (float)H;
     const float inv_mine = 1.f / (float)part_elems<NC>(H, W, part);
+    const int peer = lane & 15;                       // the part of the row that this lane joins
+    const float peer_n = peer < W ? (float)part_elems<NC>(H, W, peer) : 0.f;
     const long long stride = (long long)gridDim.x * G;
     long long row = (long long)blockIdx.x * G + grp;
-    Chunk<XT> next[NC];
+    // rows in flight: each step takes the row in its slot and loads the one two steps on into it
+    Chunk<XT> slot[2][NC];
+    auto fetch = [&](Chunk<XT> (&c)[NC], long long r) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k) next[k] = load_chunk(x + row * H + col[k], row < T ? n[k] : 0);
-    int par = 0;
-    // the workgroup's rows advance together, so every wavefront meets the barrier
-    for (long long row0 = (long long)blockIdx.x * G; row0 < T; row0 += stride, row += stride, par ^= 1) {
+        for (int k = 0; k < NC; ++k) c[k] = load_chunk<TAIL>(x + r * H + col[k], r < T ? n[k] : 0);
+    };
+    if (KEEP) {
+        fetch(slot[0], row);
+        fetch(slot[1], row + stride);
+    }
+    auto step = [&](int par) {
+        Chunk<XT> (&next)[NC] = slot[par];
         const bool ok = row < T;
         float v[NC][8];
+        if (!KEEP) fetch(next, row);
 #pragma unroll
         for (int k = 0; k < NC; ++k) unpack(next[k], v[k]);
-#pragma unroll
-        for (int k = 0; k < NC; ++k)
-            next[k] = load_chunk(x + (row + stride) * H + col[k], row + stride < T ? n[k] : 0);
+        if (KEEP) fetch(next, row + 2 * stride);
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NC; ++k)
@@ -162,41 +181,32 @@ __global__ __launch_bounds__(1024) void k_layer_norm(const XT* __restrict__ x, i
             for (int i = 0; i < 8; ++i) s += v[k][i];
         // through a scalar register: m is one rounded value everywhere below (contracted into v - m, the
         // product would enter unrounded there and rounded elsewhere, and e would not be its rounding)
-        float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(wave_sum(s) * inv_mine)));
+        float m = readlane(wave_sum_dpp(s) * inv_mine, 0);
         float e = 0.f, q = 0.f;
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = i < n[k] ? v[k][i] - m : 0.f;
+                const float d = (TAIL ? i < n[k] : n[k] > 0) ? v[k][i] - m : 0.f;
                 e += d;
                 q = fmaf(d, d, q);
             }
-        e = wave_sum(e);
-        q = wave_sum(q);
+        e = wave_sum_dpp(e);
+        q = wave_sum_dpp(q);
         float delta, sq;   // mean relative to m, centred square sum of the row
         if (W == 1) {
             delta = e * inv_h;
             sq = q - e * delta;
         } else {
-            if (lane == 0) {
-                s_m[par][wave] = m;
-                s_e[par][wave] = e;
-                s_q[par][wave] = q;
-            }
-            __syncthreads();   // the other parity's readers passed the barrier before this one's writers run again
-            const int w0 = grp * W;
-            m = s_m[par][w0];
-            float sum = 0.f;
-            for (int i = 0; i < W; ++i)
-                sum += fmaf((float)part_elems<NC>(H, W, i), s_m[par][w0 + i] - m, s_e[par][w0 + i]);
-            delta = sum * inv_h;
-            sq = 0.f;
-            for (int i = 0; i < W; ++i) {
-                const float ni = (float)part_elems<NC>(H, W, i), ei = s_e[par][w0 + i];
-                const float off = (s_m[par][w0 + i] - m) - delta;      // part's m relative to the row's mean
-                sq += s_q[par][w0 + i] + off * fmaf(ni, off, 2.f * ei);
-            }
+            if (lane == 0) s_part[par][wave] = make_float4(m, e, q, 0.f);
+            // one barrier: who still reads the other parity passed its barrier before this row's writes
+            __syncthreads();
+            const float4 p = s_part[par][grp * W + (peer < W ? peer : 0)];
+            m = readlane(p.x, 0);
+            const float shift = p.x - m;
+            delta = row_sum(peer < W ? fmaf(peer_n, shift, p.y) : 0.f) * inv_h;
+            const float off = shift - delta;          // the part's m relative to the row's mean
+            sq = row_sum(peer < W ? fmaf(off, fmaf(peer_n, off, 2.f * p.y), p.z) : 0.f);
         }
         if (sq < 0.f) sq = 0.f;   // NaN stays
         const float r = 1.f / sqrtf(fmaf(sq, inv_h, eps));
@@ -204,22 +214,33 @@ __global__ __launch_bounds__(1024) void k_layer_norm(const XT* __restrict__ x, i
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
                 float o[8];
+                const int kk = KEEP ? k : 0;
+                if (!KEEP) {
+                    load_param<TAIL>(weight, wdtype, col[k] / 8, n[k], 1.f, w[0]);
+                    load_param<TAIL>(bias, wdtype, col[k] / 8, n[k], 0.f, b[0]);
+                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(((v[k][i] - m) - delta) * r, w[k][i], b[k][i]);
-                store_chunk(y + row * H + col[k], n[k], o);
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(((v[k][i] - m) - delta) * r, w[kk][i], b[kk][i]);
+                store_chunk<TAIL, STREAM>(y + row * H + col[k], n[k], o);
             }
             if (part == 0 && lane == 0) {
                 if (mean) mean[row] = m + delta;
                 if (rstd) rstd[row] = r;
             }
         }
+        row += stride;
+    };
+    // the workgroup's rows advance together, so every wavefront meets the barriers
+    for (long long row0 = (long long)blockIdx.x * G; row0 < T; row0 += 2 * stride) {
+        step(0);
+        if (row0 + stride < T) step(1);
     }
 }
 
 // Row gradients of the workgroup's rows, and its sums of gy * xh and gy per
 // column into part[2 * blockIdx][H] and part[2 * blockIdx + 1][H] (straight
 // into gw and gb when one workgroup has every row).
-template <typename XT, typename YT, int NC>
+template <typename XT, typename YT, int NC, bool TAIL>
 __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restrict__ gy, const XT* __restrict__ x,
                                                               const float* __restrict__ mean,
                                                               const float* __restrict__ rstd, int T, int H, int W,
@@ -227,7 +248,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
                                                               XT* __restrict__ gx, float* __restrict__ pw,
                                                               float* __restrict__ pb, long long pstride) {
     extern __shared__ float s_cols[];   // [2][H], G > 1 only
-    __shared__ float s_a[2][kMaxWaves], s_b[2][kMaxWaves];
+    __shared__ float2 s_part[2][kMaxWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int grp = wave / W, part = wave - grp * W;
     int col[NC], n[NC];
@@ -237,64 +258,62 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
         const int c = (part + k * W) * 64 + lane;
         col[k] = 8 * c;
         n[k] = min(max(H - col[k], 0), 8);
-        load_param(weight, wdtype, c, n[k], 1.f, w[k]);
+        load_param<TAIL>(weight, wdtype, c, n[k], 1.f, w[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) aw[k][i] = ab[k][i] = 0.f;
     }
     const float inv_h = 1.f / (float)H;
     const long long stride = (long long)gridDim.x * G;
     long long row = (long long)blockIdx.x * G + grp;
-    Chunk<XT> nx[NC];
-    Chunk<YT> ng[NC];
-    float nm = 0.f, nr = 0.f;
-    auto fetch = [&](long long r) {
+    constexpr int DEPTH = NC == 1 ? 2 : 1;   // rows in flight, as far as the registers go
+    Chunk<XT> nx[DEPTH][NC];
+    Chunk<YT> ng[DEPTH][NC];
+    float nm[DEPTH], nr[DEPTH];
+    auto fetch = [&](int d, long long r) {
         const bool ok = r < T;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            nx[k] = load_chunk(x + r * H + col[k], ok ? n[k] : 0);
-            ng[k] = load_chunk(gy + r * H + col[k], ok ? n[k] : 0);
+            nx[d][k] = load_chunk<TAIL>(x + r * H + col[k], ok ? n[k] : 0);
+            ng[d][k] = load_chunk<TAIL>(gy + r * H + col[k], ok ? n[k] : 0);
         }
-        nm = ok ? mean[r] : 0.f;
-        nr = ok ? rstd[r] : 0.f;
+        nm[d] = ok ? mean[r] : 0.f;
+        nr[d] = ok ? rstd[r] : 0.f;
     };
-    fetch(row);
-    int par = 0;
-    for (long long row0 = (long long)blockIdx.x * G; row0 < T; row0 += stride, row += stride, par ^= 1) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) fetch(d, row + d * stride);
+    auto step = [&](int par) {
+        const int d = par % DEPTH;
         const bool ok = row < T;
-        const float m = nm, r = nr;
+        const float m = nm[d], r = nr[d];
         float xh[NC][8], g[NC][8];
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            unpack(nx[k], xh[k]);
-            unpack(ng[k], g[k]);
+            unpack(nx[d][k], xh[k]);
+            unpack(ng[d][k], g[k]);
         }
-        fetch(row + stride);
+        fetch(d, row + DEPTH * stride);
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 // past the row's end gy reads as 0; xh must be 0 there too (0 * inf)
-                xh[k][i] = i < n[k] ? (xh[k][i] - m) * r : 0.f;
+                xh[k][i] = (TAIL ? i < n[k] : n[k] > 0) ? (xh[k][i] - m) * r : 0.f;
                 aw[k][i] = fmaf(g[k][i], xh[k][i], aw[k][i]);
                 ab[k][i] += g[k][i];
                 g[k][i] *= w[k][i];
                 a += g[k][i];
                 b = fmaf(g[k][i], xh[k][i], b);
             }
-        a = wave_sum(a);
-        b = wave_sum(b);
+        a = wave_sum_dpp(a);
+        b = wave_sum_dpp(b);
         if (W > 1) {
-            if (lane == 0) {
-                s_a[par][wave] = a;
-                s_b[par][wave] = b;
-            }
+            if (lane == 0) s_part[par][wave] = make_float2(a, b);
             __syncthreads();
-            a = b = 0.f;
-            for (int i = 0; i < W; ++i) {
-                a += s_a[par][grp * W + i];
-                b += s_b[par][grp * W + i];
-            }
+            const int peer = lane & 15;
+            const float2 p = s_part[par][grp * W + (peer < W ? peer : 0)];
+            a = row_sum(peer < W ? p.x : 0.f);
+            b = row_sum(peer < W ? p.y : 0.f);
         }
         a *= inv_h;
         b *= inv_h;
@@ -304,9 +323,14 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = r * (g[k][i] - a - xh[k][i] * b);
-                store_chunk(gx + row * H + col[k], n[k], o);
+                store_chunk<TAIL>(gx + row * H + col[k], n[k], o);
             }
         }
+        row += stride;
+    };
+    for (long long row0 = (long long)blockIdx.x * G; row0 < T; row0 += 2 * stride) {
+        step(0);
+        if (row0 + stride < T) step(1);
     }
     if (!pw && !pb) return;
     if (G > 1) {   // the row groups' columns, one group after the other
@@ -332,33 +356,55 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
     }
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        if (pw) store_chunk(pw + (long long)blockIdx.x * pstride + col[k], n[k], aw[k]);
-        if (pb) store_chunk(pb + (long long)blockIdx.x * pstride + col[k], n[k], ab[k]);
+        if (pw) store_chunk<TAIL>(pw + (long long)blockIdx.x * pstride + col[k], n[k], aw[k]);
+        if (pb) store_chunk<TAIL>(pb + (long long)blockIdx.x * pstride + col[k], n[k], ab[k]);
     }
 }
 
 // gw / gb = sum over the nb workgroups' partials [nb][2][H], in a fixed order
-// (no atomics, so a call repeats bit for bit): 32 columns x 8 slices of the
-// partials per workgroup.  nb = 0 (no rows) writes zeros.
+// (no atomics, so a call repeats bit for bit): 64 columns x 16 slices of the
+// partials per workgroup, four columns per lane, four partials in flight.
+// nb = 0 (no rows) writes zeros.
 __global__ __launch_bounds__(256) void k_norm_param_grads(const float* __restrict__ part, int nb, int H,
                                                           float* __restrict__ gw, float* __restrict__ gb) {
-    __shared__ float s[8][33];
-    const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const long long c = (long long)blockIdx.x * 32 + cl;   // column of [2][H]
-    float v = 0.f;
-    if (c < 2ll * H)
-        for (int i = sl; i < nb; i += 8) v += part[(long long)i * 2 * H + c];
-    s[sl][cl] = v;
-    __syncthreads();
-    if (sl == 0 && c < 2ll * H) {
-        float o = 0.f;
+    __shared__ float s[16][64];
+    const int cl = (threadIdx.x & 15) * 4, sl = threadIdx.x >> 4;
+    const int c = blockIdx.x * 64 + cl;   // column of [2][H]
+    const int n = min(max(2 * H - c, 0), 4);
+    const long long stride = 2ll * H;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = sl; i0 < nb; i0 += 64) {
+        float f[4][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o += s[i][cl];
-        if (c < H) {
-            if (gw) gw[c] = o;
-        } else if (gb) {
-            gb[c - H] = o;
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + 16 * u;
+            const float* p = part + i * stride + c;
+            if (i < nb && n == 4) {
+                const u32x4 w = *(const u32x4_e*)p;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[u][k] = __uint_as_float(w[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[u][k] = i < nb && k < n ? p[k] : 0.f;
+            }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] += f[u][k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[sl][cl + k] = v[k];
+    __syncthreads();
+    const int h = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x >= 64 || h >= 2 * H) return;
+    float o = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o += s[i][threadIdx.x];
+    if (h < H) {
+        if (gw) gw[h] = o;
+    } else if (gb) {
+        gb[h - H] = o;
     }
 }
 
@@ -366,20 +412,42 @@ constexpr int kMaxRowElems = 64 * 8 * kMaxWaves * 4;   // 4 steps of 16 wavefron
 static_assert(kMaxRowElems == MOE_NORM_MAX_H, "norm row limit");
 constexpr int kBackwardBlocks = 256;                   // one workgroup per CU walks the rows
 
-// Steps per lane and wavefronts per row.
-void row_shape(int H, int* NC, int* W) {
+// Steps per lane and wavefronts per row: at most `wide` wavefronts share a row
+// while 2 steps do.
+void row_shape(int H, int wide, int* NC, int* W) {
     const int groups = (H + 511) / 512;   // 64-lane groups of chunks
-    *NC = groups <= kMaxWaves ? 1 : groups <= 2 * kMaxWaves ? 2 : 4;
+    *NC = groups <= wide ? 1 : groups <= 2 * kMaxWaves ? 2 : 4;
     *W = (groups + *NC - 1) / *NC;
 }
+constexpr int kForwardWide = 8, kBackwardWide = kMaxWaves;
 
 int backward_blocks(int T, int G) { return min(kBackwardBlocks, (int)(((long long)T + G - 1) / G)); }
+
+// Calls go with the row types, the steps per lane and whether rows end inside
+// a chunk.
+template <typename F>
+void by_variant(int x_dtype, int y_dtype, int NC, int H, F go) {
+    auto by_nc = [&](auto xt, auto yt) {
+        auto by_tail = [&](auto nc) {
+            if (H % 8) go(xt, yt, nc, std::true_type{});
+            else go(xt, yt, nc, std::false_type{});
+        };
+        if (NC == 1) by_tail(std::integral_constant<int, 1>{});
+        else if (NC == 2) by_tail(std::integral_constant<int, 2>{});
+        else by_tail(std::integral_constant<int, 4>{});
+    };
+    const bool xb = x_dtype == MOE_BF16, yb = y_dtype == MOE_BF16;
+    if (xb && yb) by_nc(uint16_t{}, uint16_t{});
+    else if (xb) by_nc(uint16_t{}, float{});
+    else if (yb) by_nc(float{}, uint16_t{});
+    else by_nc(float{}, float{});
+}
 
 }  // namespace
 
 size_t norm_backward_scratch_bytes(int T, int H) {
     int NC, W;
-    row_shape(H, &NC, &W);
+    row_shape(H, kBackwardWide, &NC, &W);
     return (size_t)backward_blocks(T, kMaxWaves / W) * 2 * H * sizeof(float);
 }
 
@@ -388,27 +456,26 @@ hipError_t launch_layer_norm(int T, int H, int x_dtype, int y_dtype, int w_dtype
                              hipStream_t s) {
     if (T == 0) return hipSuccess;
     int NC, W;
-    row_shape(H, &NC, &W);
+    row_shape(H, kForwardWide, &NC, &W);
     const int G = W >= 4 ? 1 : 4 / W;
     const int per_cu = max(1, 32 / (W * G));
+    // outputs past the 32 MB of L2 leave it anyway: nontemporal stores, 8192 x 7168 bf16 in 43.6 us against 55.8
+    // (5.4 and 4.2 TB/s); smaller ones stay for the router's product and the dispatch that read them next
+    const bool stream = (long long)T * H * (y_dtype == MOE_BF16 ? 2 : 4) > (32ll << 20);
     const long long want = ((long long)T + G - 1) / G, most = (long long)num_cu * per_cu;
     const unsigned grid = (unsigned)(want < most ? want : most);
-    auto go = [&](auto xt, auto yt, auto nc) {
+    auto go = [&](auto xt, auto yt, auto nc, auto tail) {
         using XT = decltype(xt);
         using YT = decltype(yt);
-        hipLaunchKernelGGL((k_layer_norm<XT, YT, decltype(nc)::value>), dim3(grid), dim3(64 * W * G), 0, s,
-                           (const XT*)x, T, H, W, G, weight, bias, w_dtype, eps, (YT*)y, mean, rstd);
+        auto launch = [&](auto st) {
+            hipLaunchKernelGGL((k_layer_norm<XT, YT, decltype(nc)::value, decltype(tail)::value, decltype(st)::value>),
+                               dim3(grid), dim3(64 * W * G), 0, s, (const XT*)x, T, H, W, G, weight, bias, w_dtype,
+                               eps, (YT*)y, mean, rstd);
+        };
+        if (stream) launch(std::true_type{});
+        else launch(std::false_type{});
     };
-    auto by_nc = [&](auto xt, auto yt) {
-        if (NC == 1) go(xt, yt, std::integral_constant<int, 1>{});
-        else if (NC == 2) go(xt, yt, std::integral_constant<int, 2>{});
-        else go(xt, yt, std::integral_constant<int, 4>{});
-    };
-    const bool xb = x_dtype == MOE_BF16, yb = y_dtype == MOE_BF16;
-    if (xb && yb) by_nc(uint16_t{}, uint16_t{});
-    else if (xb) by_nc(uint16_t{}, float{});
-    else if (yb) by_nc(float{}, uint16_t{});
-    else by_nc(float{}, float{});
+    by_variant(x_dtype, y_dtype, NC, H, go);
     return hipGetLastError();
 }
 
@@ -416,7 +483,7 @@ hipError_t launch_layer_norm_backward(int T, int H, int x_dtype, int y_dtype, in
                                       const void* x, const float* mean, const float* rstd, const void* weight,
                                       void* gx, float* gw, float* gb, void* scratch, hipStream_t s) {
     int NC, W;
-    row_shape(H, &NC, &W);
+    row_shape(H, kBackwardWide, &NC, &W);
     const int G = kMaxWaves / W;
     const int nb = T > 0 ? backward_blocks(T, G) : 0;
     const bool params = gw || gb;
@@ -425,28 +492,19 @@ hipError_t launch_layer_norm_backward(int T, int H, int x_dtype, int y_dtype, in
         float* pw = nb == 1 ? gw : params ? part : nullptr;
         float* pb = nb == 1 ? gb : params ? part + H : nullptr;
         const size_t lds = params && G > 1 ? (size_t)2 * H * sizeof(float) : 0;
-        auto go = [&](auto xt, auto yt, auto nc) {
+        auto go = [&](auto xt, auto yt, auto nc, auto tail) {
             using XT = decltype(xt);
             using YT = decltype(yt);
-            hipLaunchKernelGGL((k_layer_norm_backward<XT, YT, decltype(nc)::value>), dim3(nb), dim3(64 * W * G), lds,
+            hipLaunchKernelGGL((k_layer_norm_backward<XT, YT, decltype(nc)::value, decltype(tail)::value>), dim3(nb), dim3(64 * W * G), lds,
                                s, (const YT*)gy, (const XT*)x, mean, rstd, T, H, W, G, weight, w_dtype, (XT*)gx, pw,
                                pb, 2ll * H);
         };
-        auto by_nc = [&](auto xt, auto yt) {
-            if (NC == 1) go(xt, yt, std::integral_constant<int, 1>{});
-            else if (NC == 2) go(xt, yt, std::integral_constant<int, 2>{});
-            else go(xt, yt, std::integral_constant<int, 4>{});
-        };
-        const bool xb = x_dtype == MOE_BF16, yb = y_dtype == MOE_BF16;
-        if (xb && yb) by_nc(uint16_t{}, uint16_t{});
-        else if (xb) by_nc(uint16_t{}, float{});
-        else if (yb) by_nc(float{}, uint16_t{});
-        else by_nc(float{}, float{});
+        by_variant(x_dtype, y_dtype, NC, H, go);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || nb == 1) return e;
     }
     if (!params) return hipSuccess;
-    hipLaunchKernelGGL(k_norm_param_grads, dim3((unsigned)((2ll * H + 31) / 32)), dim3(256), 0, s,
+    hipLaunchKernelGGL(k_norm_param_grads, dim3((unsigned)((2 * H + 63) / 64)), dim3(256), 0, s,
                        (const float*)scratch, nb, H, gw, gb);
     return hipGetLastError();
 }
