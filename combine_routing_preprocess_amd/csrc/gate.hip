@@ -13,135 +13,286 @@
 //     sigmoid, normalised   gl_j = scale * q_j * (1 - s_j) * (G_j - sum_i G_i q_i)
 //
 // One wavefront per token; lane l holds experts l, l + 64, ... (EPL of them).
-// Keys are 64-bit floats: score + bias decides between experts that 32 bits
-// cannot tell apart, and the choice is an integer that must not hang on a
-// rounding.  Scores are held as their logarithm (l - m for the softmax,
-// log sigmoid otherwise), so that the normalised weights, a softmax over the
-// chosen logarithms, stay finite where every chosen score underflows.
-#include "moe_internal.h"
+// Neither direction moves many bytes (a row of logits, K weights): the time
+// goes into the K selection rounds and the 64-bit scores, so that is what the
+// layout is for.
+//  * With a bias the keys are 64-bit floats: score + bias decides between
+//    experts that 32 bits cannot tell apart, and the choice is an integer that
+//    must not hang on a rounding.  Without one the logits themselves rank the
+//    experts, exactly.  Either way a key becomes an unsigned integer of the
+//    same order; a round takes the maximum of the upper 32 bits over the lanes
+//    (lane permutes, no LDS), ballots find who holds it, and the lower 32 bits
+//    are looked at only where several do.  The winner is scalar, so lane j
+//    keeps slot j's expert and logit without any exchange.
+//  * exp and the reciprocal below are for arguments that occur here (x <= 0
+//    and 1 <= d <= 2) and take 18 and 6 instructions instead of the library's
+//    general forms.
+#include "wave_ops.h"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
-}
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
-    return v;
+using namespace ops;
+
+constexpr double kOut = -INFINITY;   // logit or key of an expert that is no candidate
+constexpr double kTiny = 1e-280;     // sums of sigmoids below this are formed from logarithms
+
+// exp(x) for x <= 0 (0 for NaN): x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in
+// two parts), the Taylor polynomial of degree 13 at r (next term 4e-18),
+// scaled by 2^n.
+__device__ __forceinline__ double exp_neg(double x) {
+    x = fmax(x, -1100.0);
+    const double n = rint(x * 1.4426950408889634);
+    double r = fma(n, -0x1.62e42fefa3800p-1, x);      // the upper 42 bits of ln 2: n times it is exact
+    r = fma(n, -0x1.ef35793c76730p-45, r);
+    double p = 1.0 / 6227020800.0;
+    p = fma(p, r, 1.0 / 479001600.0);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
-constexpr double kOut = -INFINITY;   // key of an expert that is not (or no longer) a candidate
+// sigmoid(l) and sigmoid(-l): with e = exp(-|l|), 1 / (1 + e) and e / (1 + e);
+// the reciprocal from the hardware's estimate by two Newton steps.
+__device__ __forceinline__ void sigmoids(double l, double* s, double* other) {
+    const double e = exp_neg(-fabs(l)), d = 1.0 + e;
+    double y = __builtin_amdgcn_rcp(d);
+    y = fma(y, fma(-d, y, 1.0), y);
+    y = fma(y, fma(-d, y, 1.0), y);
+    const double z = e * y;
+    *s = l < 0.0 ? z : y;
+    *other = l < 0.0 ? y : z;
+}
+__device__ __forceinline__ double sigmoid_of(double l) {
+    double s, o;
+    sigmoids(l, &s, &o);
+    return s;
+}
+__device__ __forceinline__ double log_sigmoid(double l) { return fmin(l, 0.0) - log1p(exp(-fabs(l))); }
 
+// A logit as a float (exact); NaN reads as no candidate, -0 as 0.
 template <typename LT>
-__device__ __forceinline__ double load_logit(const LT* p) {
-    if constexpr (sizeof(LT) == 2) return (double)__uint_as_float((uint32_t)*p << 16);
-    else return (double)*p;
+__device__ __forceinline__ float load_logit(const LT* p) {
+    float v;
+    if constexpr (sizeof(LT) == 2) v = __uint_as_float((uint32_t)*p << 16);
+    else v = *p;
+    return v == v ? v + 0.f : -INFINITY;
 }
 
-// Logarithm of the score, up to the row's constant in the softmax case.
-__device__ __forceinline__ double log_score(double l, int sigmoid) {
-    return sigmoid ? fmin(l, 0.0) - log1p(exp(-fabs(l))) : l;
+// Unsigned integers in the order of the floats (all above 0 but -inf and NaN,
+// which the callers leave out).
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
 }
 
-// Logits of a lane's experts (NaN and experts past E read as kOut), and the
-// row's maximum and sum of exp(l - max) for the softmax.
-template <typename LT, int EPL>
-__device__ __forceinline__ void load_row(const LT* row, int E, int lane, int sigmoid, double (&l)[EPL], double* m,
-                                         double* sum) {
-    *m = kOut;
+// Maximum of the row's logits and the sum of exp(l - max) (softmax).
+template <int EPL>
+__device__ __forceinline__ void softmax_terms(const float (&l)[EPL], double* m, double* sum) {
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) top = fmaxf(top, l[i]);
+    *m = wave_max_dpp((double)top);
+    double a = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) a += l[i] == -INFINITY ? 0.0 : exp_neg((double)l[i] - *m);
+    *sum = wave_sum_dpp(a);
+}
+
+// One choice per round for up to 64 slots: on return lane j < n holds slot j's
+// expert and logit, and taken[i] says in which slot the lane's expert i is.
+template <typename LT, int EPL, bool BIAS>
+__device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, int E, int K, int sigmoid, double m,
+                                      double sum, int lane, int* my_e, float* my_l, int (&taken)[EPL]) {
+    uint32_t hi[EPL], lo[BIAS ? EPL : 1];
+    const double inv = BIAS && !sigmoid ? 1.0 / sum : 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = lane + 64 * i;
-        l[i] = e < E ? load_logit(row + e) : kOut;
-        if (!(l[i] == l[i])) l[i] = kOut;
-        *m = fmax(*m, l[i]);
+        taken[i] = -1;
+        hi[i] = 0u;
+        if constexpr (BIAS) {
+            lo[i] = 0u;
+            if (e < E) {
+                const double s = sigmoid ? sigmoid_of((double)l[i]) : exp_neg((double)l[i] - m) * inv;
+                const double key = s + (double)bias[e] + 0.0;
+                if (l[i] != -INFINITY && key > kOut) {
+                    const uint64_t u = ordered(key);
+                    hi[i] = (uint32_t)(u >> 32);
+                    lo[i] = (uint32_t)u;
+                }
+            }
+        } else if (l[i] != -INFINITY) {
+            hi[i] = ordered(l[i]);
+        }
     }
-    *sum = 1.0;
-    if (sigmoid) return;
-    *m = wave_max(*m);
-    double a = 0.0;
-    if (*m != kOut) {
+    int n = 0;
+    for (; n < K; ++n) {
+        uint32_t top = hi[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = max(top, hi[i]);
+        top = wave_max_dpp(top);
+        if (top == 0u) break;   // no candidate is left
+        uint64_t has[EPL];
+        int holders = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            has[i] = __ballot(hi[i] == top);
+            holders += __popcll(has[i]);
+        }
+        if (BIAS && holders > 1) {
+            uint32_t low = 0u;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) low = max(low, hi[i] == top ? lo[BIAS ? i : 0] : 0u);
+            low = wave_max_dpp(low);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) has[i] = __ballot(hi[i] == top && lo[BIAS ? i : 0] == low);
+        }
+        bool found = false;   // the lowest expert: lowest i, then lowest lane
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (l[i] != kOut) a += exp(l[i] - *m);
+            if (!found && has[i]) {
+                found = true;
+                const int at = __ffsll((unsigned long long)has[i]) - 1;
+                const float v = readlane(l[i], at);
+                if (lane == n) {
+                    *my_e = at + 64 * i;
+                    *my_l = v;
+                }
+                if (lane == at) {
+                    taken[i] = n;
+                    hi[i] = 0u;
+                }
+            }
     }
-    *sum = wave_sum(a);
+    return n;
 }
 
-template <typename LT, int FMT, int EPL>
+// K <= 64: a slot per lane.
+template <typename LT, int FMT, int EPL, bool BIAS>
 __global__ __launch_bounds__(256) void k_gate(const LT* __restrict__ logits, int T, int E, int K,
                                               const float* __restrict__ bias, int sigmoid, int normalize, float scale,
                                               void* __restrict__ routing, float* __restrict__ probs) {
     const int lane = threadIdx.x & 63;
     const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
-    double l[EPL], key[EPL], m, sum;
-    int slot[EPL];
-    load_row<LT, EPL>(logits + t * E, E, lane, sigmoid, l, &m, &sum);
+    float l[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = l[i];
-        if (bias && l[i] != kOut) {
-            const double s = sigmoid ? 1.0 / (1.0 + exp(-l[i])) : exp(l[i] - m) / sum;
-            key[i] = s + (double)bias[e];
-            if (!(key[i] == key[i])) key[i] = kOut;
-        }
-        slot[i] = -1;
-    }
-    int n = 0;   // chosen so far
-    for (; n < K; ++n) {
-        double best = kOut;
-        int at = 1 << 30;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 64 * i;
-            }
-#pragma unroll
-        for (int x = 32; x >= 1; x >>= 1) {
-            const double ob = __shfl_xor(best, x, 64);
-            const int oa = __shfl_xor(at, x, 64);
-            if (ob > best || (ob == best && oa < at)) {
-                best = ob;
-                at = oa;
+    for (int i = 0; i < EPL; ++i) l[i] = lane + 64 * i < E ? load_logit(logits + t * E + lane + 64 * i) : -INFINITY;
+    double m = 0.0, sum = 1.0;
+    if (!sigmoid && (BIAS || !normalize)) softmax_terms<EPL>(l, &m, &sum);
+    int my_e = -1, taken[EPL];
+    float my_l = -INFINITY;
+    const int n = choose<LT, EPL, BIAS>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken);
+    // weight of the lane's slot
+    double w = 0.0;
+    if (sigmoid) {
+        w = lane < n ? sigmoid_of((double)my_l) : 0.0;
+        if (normalize) {
+            sum = wave_sum_dpp(w);
+            if (sum < kTiny) {   // the same for every lane
+                const double ls = lane < n ? log_sigmoid((double)my_l) : kOut;
+                const double top = wave_max_dpp(ls);
+                w = lane < n ? exp(ls - top) : 0.0;
+                sum = wave_sum_dpp(w);
             }
         }
-        if (best == kOut) break;   // the same for every lane
+    } else {
+        if (normalize) m = wave_max_dpp((double)my_l);
+        w = lane < n ? exp_neg((double)my_l - m) : 0.0;
+        if (normalize) sum = wave_sum_dpp(w);
+    }
+    const float p = lane < n ? (float)(w * ((double)scale / sum)) : 0.f;
+    if constexpr (FMT == MOE_ROUTE_SPARSE_BOOL) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + 64 * i;
+            const float pe = __shfl(p, taken[i] & 63, 64);
+            if (e < E) {
+                ((uint8_t*)routing)[t * E + e] = taken[i] >= 0;
+                probs[t * E + e] = taken[i] >= 0 ? pe : 0.f;
+            }
+        }
+    } else if (lane < K) {
+        using IT = std::conditional_t<FMT == MOE_ROUTE_DENSE_I16, int16_t, int32_t>;
+        ((IT*)routing)[t * K + lane] = (IT)my_e;
+        probs[t * K + lane] = p;
+    }
+}
+
+// Any K: slots stay with the experts' lanes.
+template <typename LT, int FMT, int EPL>
+__global__ __launch_bounds__(256) void k_gate_many(const LT* __restrict__ logits, int T, int E, int K,
+                                                   const float* __restrict__ bias, int sigmoid, int normalize,
+                                                   float scale, void* __restrict__ routing,
+                                                   float* __restrict__ probs) {
+    const int lane = threadIdx.x & 63;
+    const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    float l[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = lane + 64 * i < E ? load_logit(logits + t * E + lane + 64 * i) : -INFINITY;
+    double m = 0.0, sum = 1.0;
+    if (!sigmoid && (bias || !normalize)) softmax_terms<EPL>(l, &m, &sum);
+    int my_e = -1, taken[EPL];
+    float my_l = -INFINITY;
+    const int n = bias ? choose<LT, EPL, true>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken)
+                       : choose<LT, EPL, false>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken);
+    double w[EPL], part = 0.0;
+    if (normalize && !sigmoid) {
+        m = kOut;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (at == lane + 64 * i) {
-                slot[i] = n;
-                key[i] = kOut;
-            }
+            if (taken[i] >= 0) m = fmax(m, (double)l[i]);
+        m = wave_max_dpp(m);
     }
-    // weights of the chosen
-    double top = kOut, part = 0.0, w[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        w[i] = slot[i] >= 0 ? log_score(l[i], sigmoid) : kOut;
-        top = fmax(top, w[i]);
-    }
-    if (normalize) top = wave_max(top);
-    else top = sigmoid ? 0.0 : m;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        w[i] = slot[i] >= 0 ? exp(w[i] - top) : 0.0;
+        w[i] = 0.0;
+        if (taken[i] >= 0) w[i] = sigmoid ? sigmoid_of((double)l[i]) : exp_neg((double)l[i] - m);
         part += w[i];
     }
-    const double f = (double)scale / (normalize ? wave_sum(part) : sum);
+    if (normalize) {
+        sum = wave_sum_dpp(part);
+        if (sigmoid && sum < kTiny) {
+            double top = kOut;
+            part = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                w[i] = taken[i] >= 0 ? log_sigmoid((double)l[i]) : kOut;
+                top = fmax(top, w[i]);
+            }
+            top = wave_max_dpp(top);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                w[i] = taken[i] >= 0 ? exp(w[i] - top) : 0.0;
+                part += w[i];
+            }
+            sum = wave_sum_dpp(part);
+        }
+    }
+    const double f = (double)scale / sum;
     if constexpr (FMT == MOE_ROUTE_SPARSE_BOOL) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 64 * i;
             if (e < E) {
-                ((uint8_t*)routing)[t * E + e] = slot[i] >= 0;
-                probs[t * E + e] = slot[i] >= 0 ? (float)(w[i] * f) : 0.f;
+                ((uint8_t*)routing)[t * E + e] = taken[i] >= 0;
+                probs[t * E + e] = taken[i] >= 0 ? (float)(w[i] * f) : 0.f;
             }
         }
     } else {
@@ -150,9 +301,9 @@ __global__ __launch_bounds__(256) void k_gate(const LT* __restrict__ logits, int
         float* p = probs + t * K;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (slot[i] >= 0) {
-                idx[slot[i]] = (IT)(lane + 64 * i);
-                p[slot[i]] = (float)(w[i] * f);
+            if (taken[i] >= 0) {
+                idx[taken[i]] = (IT)(lane + 64 * i);
+                p[taken[i]] = (float)(w[i] * f);
             }
         for (int j = n + lane; j < K; j += 64) {
             idx[j] = (IT)-1;
@@ -161,20 +312,89 @@ __global__ __launch_bounds__(256) void k_gate(const LT* __restrict__ logits, int
     }
 }
 
-template <typename LT, int FMT, int EPL>
+template <typename LT>
+__device__ __forceinline__ void store_grad(LT* p, double v) {
+    if constexpr (sizeof(LT) == 2) *p = (LT)f32_to_bf16((float)v);
+    else *p = (float)v;
+}
+
+// Dense routing, K <= 64: lane j has slot j.  Only the chosen experts' logits
+// are read, but for the softmax over the whole row.
+template <typename LT, typename IT, int EPL>
 __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__ grad_probs,
-                                                       const LT* __restrict__ logits,
-                                                       const void* __restrict__ routing, int T, int E, int K,
-                                                       int sigmoid, int normalize, float scale,
+                                                       const LT* __restrict__ logits, const IT* __restrict__ routing,
+                                                       int T, int E, int K, int sigmoid, int normalize, float scale,
                                                        LT* __restrict__ grad_logits) {
     const int lane = threadIdx.x & 63;
     const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
-    double l[EPL], g[EPL], m, sum;
+    const LT* row = logits + t * E;
+    const int e = lane < K ? (int)routing[t * K + lane] : -1;
+    float le = -INFINITY;
+    if (e >= 0 && e < E) le = load_logit(row + e);
+    const bool on = le != -INFINITY;
+    const double g = on ? (double)grad_probs[t * K + lane] : 0.0;
+    double m = 0.0, sum = 1.0, o[EPL];
+    const bool whole = !sigmoid && !normalize;
+    float l[EPL];
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = lane + 64 * i < E ? load_logit(row + lane + 64 * i) : -INFINITY;
+        softmax_terms<EPL>(l, &m, &sum);
+    } else if (!sigmoid) {
+        m = wave_max_dpp((double)le);
+    }
+    double p = 0.0, rest = 1.0;   // the slot's score or share, and 1 - score of a sigmoid
+    if (sigmoid) sigmoids((double)le, &p, &rest);
+    else p = exp_neg((double)le - m);
+    if (!on) p = 0.0;
+    if (normalize) {
+        sum = wave_sum_dpp(p);
+        if (sigmoid && sum < kTiny) {
+            const double ls = on ? log_sigmoid((double)le) : kOut, top = wave_max_dpp(ls);
+            p = on ? exp(ls - top) : 0.0;
+            sum = wave_sum_dpp(p);
+        }
+    }
+    const double inv = 1.0 / sum;
+    p = on ? p * inv : 0.0;
+    double dot = 0.0;
+    if (!sigmoid || normalize) dot = wave_sum_dpp(g * p);
+    const double v = on ? p * rest * (whole ? g : g - dot) * (double)scale : 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        o[i] = whole && l[i] != -INFINITY ? -dot * (exp_neg((double)l[i] - m) * inv) * (double)scale : 0.0;
+    // the slots' gradients to their experts, one after the other (a repeated expert adds)
+    for (int j = 0; j < K; ++j) {
+        const int ej = (int)readlane((uint32_t)e, j);
+        if (ej < 0 || ej >= E) continue;
+        const double vj = readlane(v, j);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (ej >> 6 == i) o[i] += lane == (ej & 63) ? vj : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (lane + 64 * i < E) store_grad(grad_logits + t * E + lane + 64 * i, o[i]);
+}
+
+// Boolean map, or any K: slots counted at the experts' lanes.
+template <typename LT, int FMT, int EPL>
+__global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restrict__ grad_probs,
+                                                            const LT* __restrict__ logits,
+                                                            const void* __restrict__ routing, int T, int E, int K,
+                                                            int sigmoid, int normalize, float scale,
+                                                            LT* __restrict__ grad_logits) {
+    const int lane = threadIdx.x & 63;
+    const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    float l[EPL];
+    double g[EPL];
     int cnt[EPL];   // slots that hold this expert (a repeated index adds its slots)
-    load_row<LT, EPL>(logits + t * E, E, lane, sigmoid, l, &m, &sum);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 64 * i;
+        l[i] = e < E ? load_logit(logits + t * E + e) : -INFINITY;
         g[i] = 0.0;
         cnt[i] = 0;
     }
@@ -182,7 +402,7 @@ __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 64 * i;
-            if (e < E && l[i] != kOut && ((const uint8_t*)routing)[t * E + e]) {
+            if (e < E && l[i] != -INFINITY && ((const uint8_t*)routing)[t * E + e]) {
                 cnt[i] = 1;
                 g[i] = (double)grad_probs[t * E + e];
             }
@@ -198,11 +418,11 @@ __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__
             }
             const int nj = min(64, K - j0);
             for (int j = 0; j < nj; ++j) {
-                const int e = __shfl(my, j, 64);
-                const float ge = __shfl(mg, j, 64);
+                const int e = (int)readlane((uint32_t)my, j);
+                const float ge = readlane(mg, j);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (e == lane + 64 * i && l[i] != kOut) {
+                    if (e == lane + 64 * i && l[i] != -INFINITY) {
                         ++cnt[i];
                         g[i] += (double)ge;
                     }
@@ -210,41 +430,61 @@ __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__
         }
     }
     // p = scores (or the chosen scores' shares), dot = sum over the slots of G p
-    double top = kOut, p[EPL];
+    double m = 0.0, sum = 1.0, p[EPL], rest[EPL], part = 0.0;
+    if (!sigmoid && !normalize) {
+        softmax_terms<EPL>(l, &m, &sum);
+    } else if (!sigmoid) {
+        m = kOut;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        p[i] = normalize && !cnt[i] ? kOut : log_score(l[i], sigmoid);
-        if (l[i] == kOut) p[i] = kOut;
-        if (p[i] != kOut) top = fmax(top, p[i]);
+        for (int i = 0; i < EPL; ++i)
+            if (cnt[i]) m = fmax(m, (double)l[i]);
+        m = wave_max_dpp(m);
     }
-    if (normalize) top = wave_max(top);
-    else top = sigmoid ? 0.0 : m;
-    double part = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = p[i] != kOut ? exp(p[i] - top) : 0.0;
+        p[i] = 0.0;
+        rest[i] = 1.0;
+        if (l[i] != -INFINITY && (cnt[i] || (!sigmoid && !normalize))) {
+            if (sigmoid) sigmoids((double)l[i], &p[i], &rest[i]);
+            else p[i] = exp_neg((double)l[i] - m);
+        }
         part += cnt[i] * p[i];
     }
-    const double inv = 1.0 / (normalize ? wave_sum(part) : sum);
+    if (normalize) {
+        sum = wave_sum_dpp(part);
+        if (sigmoid && sum < kTiny) {
+            double top = kOut;
+            part = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                p[i] = cnt[i] ? log_sigmoid((double)l[i]) : kOut;
+                top = fmax(top, p[i]);
+            }
+            top = wave_max_dpp(top);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                p[i] = cnt[i] ? exp(p[i] - top) : 0.0;
+                part += cnt[i] * p[i];
+            }
+            sum = wave_sum_dpp(part);
+        }
+    }
+    const double inv = 1.0 / sum;
     double dot = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         p[i] = p[i] != 0.0 ? p[i] * inv : 0.0;
         dot += g[i] * p[i];
     }
-    if (normalize || !sigmoid) dot = wave_sum(dot);
-    else dot = 0.0;
+    dot = !sigmoid || normalize ? wave_sum_dpp(dot) : 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = lane + 64 * i;
         if (e >= E) continue;
         // a slot's own gradient less, through the sum that divides it, the dot:
         // with the chosen scores' sum each slot of the expert carries it once
-        double o = p[i] * (g[i] - (normalize ? cnt[i] : 1) * dot);
-        if (sigmoid) o *= 1.0 / (1.0 + exp(l[i]));   // 1 - s
-        o = p[i] != 0.0 ? o * (double)scale : 0.0;
-        if constexpr (sizeof(LT) == 2) grad_logits[t * E + e] = (LT)f32_to_bf16((float)o);
-        else grad_logits[t * E + e] = (float)o;
+        const double o = p[i] * rest[i] * (g[i] - (normalize ? cnt[i] : 1) * dot) * (double)scale;
+        store_grad(grad_logits + t * E + e, p[i] != 0.0 ? o : 0.0);
     }
 }
 
@@ -279,8 +519,14 @@ hipError_t launch_gate(const moe_handle* h, const void* logits, int logit_dtype,
     by_type(logit_dtype, d.route_fmt, [&](auto lt, auto fmt) {
         by_epl(d.E, [&](auto epl) {
             using LT = decltype(lt);
-            hipLaunchKernelGGL((k_gate<LT, decltype(fmt)::value, decltype(epl)::value>), grid, dim3(256), 0, s,
-                               (const LT*)logits, d.T, d.E, d.K, bias, sigmoid, normalize, scale, routing, probs);
+            constexpr int FMT = decltype(fmt)::value, EPL = decltype(epl)::value;
+            auto go = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (const LT*)logits, d.T, d.E, d.K, bias, sigmoid,
+                                   normalize, scale, routing, probs);
+            };
+            if (d.K > 64) go(k_gate_many<LT, FMT, EPL>);
+            else if (bias) go(k_gate<LT, FMT, EPL, true>);
+            else go(k_gate<LT, FMT, EPL, false>);
         });
     });
     return hipGetLastError();
@@ -295,8 +541,18 @@ hipError_t launch_gate_backward(const moe_handle* h, const float* grad_probs, co
     by_type(logit_dtype, d.route_fmt, [&](auto lt, auto fmt) {
         by_epl(d.E, [&](auto epl) {
             using LT = decltype(lt);
-            hipLaunchKernelGGL((k_gate_backward<LT, decltype(fmt)::value, decltype(epl)::value>), grid, dim3(256), 0,
-                               s, grad_probs, (const LT*)logits, routing, d.T, d.E, d.K, sigmoid, normalize, scale,
+            constexpr int FMT = decltype(fmt)::value, EPL = decltype(epl)::value;
+            if constexpr (FMT != MOE_ROUTE_SPARSE_BOOL) {
+                using IT = std::conditional_t<FMT == MOE_ROUTE_DENSE_I16, int16_t, int32_t>;
+                if (d.K <= 64) {
+                    hipLaunchKernelGGL((k_gate_backward<LT, IT, EPL>), grid, dim3(256), 0, s, grad_probs,
+                                       (const LT*)logits, (const IT*)routing, d.T, d.E, d.K, sigmoid, normalize,
+                                       scale, (LT*)grad_logits);
+                    return;
+                }
+            }
+            hipLaunchKernelGGL((k_gate_backward_many<LT, FMT, EPL>), grid, dim3(256), 0, s, grad_probs,
+                               (const LT*)logits, routing, d.T, d.E, d.K, sigmoid, normalize, scale,
                                (LT*)grad_logits);
         });
     });
