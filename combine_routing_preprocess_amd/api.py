@@ -78,7 +78,7 @@ def _check_rows(t, name, shape, dtypes):
 
 
 def _check_current_device(**tensors):
-    current = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else None     # a CPU tensor's is -1
     for name, t in tensors.items():
         if t is not None and t.get_device() != current:
             raise ValueError(f"{name} must live on the current GPU")
@@ -177,6 +177,7 @@ class Dispatcher:
                  out_rows: int = 0, device=None):
         L = A.lib()
         self.device = torch.device(device if device is not None else "cuda")
+        self._cuda = self.device.type == "cuda"
         self.desc = make_desc(T, H, E, K, route_fmt, payload, pad_multiple, capacity, out_rows)
         ws_bytes = int(L.moe_workspace_bytes(C.byref(self.desc)))
         if ws_bytes == 0:
@@ -223,8 +224,9 @@ class Dispatcher:
 
     # ---- checks ------------------------------------------------------------------
     def _dev(self, t: torch.Tensor, name: str):
-        if not (t.device == self.device or (t.device.type == "cuda" and self.device.type == "cuda"
-                                            and t.device.index == torch.cuda.current_device())):
+        index = t.get_device()               # -1 on the CPU
+        if not (self._cuda and index >= 0 and (index == self.device.index or index == torch.cuda.current_device())
+                or t.device == self.device):
             raise ValueError(f"{name} must live on {self.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -238,7 +240,7 @@ class Dispatcher:
             raise ValueError(f"routing shape {tuple(routing.shape)} != {shape}")
         if probs is not None:
             self._dev(probs, "probs")
-            _need(probs.dtype == torch.float32 and tuple(probs.shape) == shape, "probs must be float32 shaped like routing")
+            _need(probs.dtype == torch.float32 and probs.shape == shape, "probs must be float32 shaped like routing")
         if T_live is not None:
             self._dev(T_live, "T_live")
             _need(T_live.dtype == torch.int32 and T_live.numel() == 1, "T_live must be one int32")
@@ -263,13 +265,15 @@ class Dispatcher:
         self._check_gate(logits, score)
         if bias is not None:
             self._dev(bias, "bias")
-            _need(bias.dtype == torch.float32 and tuple(bias.shape) == (self.E,), "bias must be float32 [E]")
+            _check_rows(bias, "bias", (self.E,), _F32)
         shape = self._routing_shape()
+        given = routing is not None or probs is not None
         if routing is None:
             routing = torch.empty(shape, dtype=_ROUTING_OUT[self.route_fmt], device=self.device)
         if probs is None:
             probs = torch.empty(shape, dtype=torch.float32, device=self.device)
-        self._check_routing(routing, probs, None)
+        if given:
+            self._check_routing(routing, probs, None)
         _check_current_device(logits=logits)
         A.check(A.lib().moe_gate(C.byref(self.h), _ptr(logits), _ROW_DT[logits.dtype], _ptr(bias), _SCORE[score],
                                  1 if normalize else 0, float(scale), _ptr(routing), _ptr(probs), _stream()),
@@ -285,8 +289,9 @@ class Dispatcher:
         self._check_routing(routing, grad_probs, None)
         if out is None:
             out = torch.empty_like(logits)
-        self._dev(out, "out")
-        _need(out.dtype == logits.dtype and out.shape == logits.shape, "out must be like logits")
+        else:
+            self._dev(out, "out")
+            _need(out.dtype == logits.dtype and out.shape == logits.shape, "out must be like logits")
         _check_current_device(logits=logits)
         A.check(A.lib().moe_gate_backward(C.byref(self.h), _ptr(grad_probs), _ptr(logits), _ROW_DT[logits.dtype],
                                           _ptr(routing), _SCORE[score], 1 if normalize else 0, float(scale),

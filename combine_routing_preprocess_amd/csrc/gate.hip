@@ -21,7 +21,7 @@
 //    must not hang on a rounding.  Without one the logits themselves rank the
 //    experts, exactly.  Either way a key becomes an unsigned integer of the
 //    same order; a round takes the maximum of the upper 32 bits over the lanes
-//    (lane permutes, no LDS), ballots find who holds it, and the lower 32 bits
+//    (lane permutes, no LDS), a ballot finds who holds it, and the lower 32 bits
 //    are looked at only where several do.  The winner is scalar, so lane j
 //    keeps slot j's expert and logit without any exchange.
 //  * exp and the reciprocal below are for arguments that occur here (x <= 0
@@ -113,31 +113,33 @@ __device__ __forceinline__ void softmax_terms(const float (&l)[EPL], double* m, 
     *sum = wave_sum_dpp(a);
 }
 
-// One choice per round for up to 64 slots: on return lane j < n holds slot j's
-// expert and logit, and taken[i] says in which slot the lane's expert i is.
-template <typename LT, int EPL, bool BIAS>
-__device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, int E, int K, int sigmoid, double m,
-                                      double sum, int lane, int* my_e, float* my_l, int (&taken)[EPL]) {
-    uint32_t hi[EPL], lo[BIAS ? EPL : 1];
-    const double inv = BIAS && !sigmoid ? 1.0 / sum : 0.0;
+// The K choices, one per round.  On return lane j < n holds slot j's expert
+// (the first 64), and with TAKEN taken[i] says in which slot the lane's expert
+// i is.  Who holds the round's largest key is looked up by ballots, so that
+// this work is scalar: ordering each lane's experts first, for rounds that
+// look at the lanes' heads only, took 14.4 us against 11.2 at 8192 x 256.
+template <int EPL, bool BIAS, bool SIGMOID, bool TAKEN>
+__device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, int E, int K, double m, double sum,
+                                      int lane, int* my_e, int (&taken)[EPL]) {
+    uint32_t hi[EPL], lo[EPL];
+    const double inv = BIAS && !SIGMOID ? 1.0 / sum : 0.0;
+    float be[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 64 * i;
-        taken[i] = -1;
-        hi[i] = 0u;
+        if (BIAS) be[i] = bias[min(lane + 64 * i, E - 1)];
+        if (TAKEN) taken[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        lo[i] = 0u;
         if constexpr (BIAS) {
-            lo[i] = 0u;
-            if (e < E) {
-                const double s = sigmoid ? sigmoid_of((double)l[i]) : exp_neg((double)l[i] - m) * inv;
-                const double key = s + (double)bias[e] + 0.0;
-                if (l[i] != -INFINITY && key > kOut) {
-                    const uint64_t u = ordered(key);
-                    hi[i] = (uint32_t)(u >> 32);
-                    lo[i] = (uint32_t)u;
-                }
-            }
-        } else if (l[i] != -INFINITY) {
-            hi[i] = ordered(l[i]);
+            const double s = SIGMOID ? sigmoid_of((double)l[i]) : exp_neg((double)l[i] - m) * inv;
+            const double key = s + (double)be[i] + 0.0;
+            const uint64_t u = l[i] != -INFINITY && key > kOut ? ordered(key) : 0u;
+            hi[i] = (uint32_t)(u >> 32);
+            lo[i] = (uint32_t)u;
+        } else {
+            hi[i] = l[i] != -INFINITY ? ordered(l[i]) : 0u;
         }
     }
     int n = 0;
@@ -148,19 +150,20 @@ __device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, 
         top = wave_max_dpp(top);
         if (top == 0u) break;   // no candidate is left
         uint64_t has[EPL];
-        int holders = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            has[i] = __ballot(hi[i] == top);
-            holders += __popcll(has[i]);
-        }
-        if (BIAS && holders > 1) {
-            uint32_t low = 0u;
+        for (int i = 0; i < EPL; ++i) has[i] = __ballot(hi[i] == top);
+        if (BIAS) {   // several holders: the lower halves decide
+            int holders = 0;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) low = max(low, hi[i] == top ? lo[BIAS ? i : 0] : 0u);
-            low = wave_max_dpp(low);
+            for (int i = 0; i < EPL; ++i) holders += __popcll(has[i]);
+            if (holders > 1) {
+                uint32_t low = 0u;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) has[i] = __ballot(hi[i] == top && lo[BIAS ? i : 0] == low);
+                for (int i = 0; i < EPL; ++i) low = max(low, hi[i] == top ? lo[i] : 0u);
+                low = wave_max_dpp(low);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) has[i] = __ballot(hi[i] == top && lo[i] == low);
+            }
         }
         bool found = false;   // the lowest expert: lowest i, then lowest lane
 #pragma unroll
@@ -168,13 +171,9 @@ __device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, 
             if (!found && has[i]) {
                 found = true;
                 const int at = __ffsll((unsigned long long)has[i]) - 1;
-                const float v = readlane(l[i], at);
-                if (lane == n) {
-                    *my_e = at + 64 * i;
-                    *my_l = v;
-                }
+                if (lane == n) *my_e = at + 64 * i;
                 if (lane == at) {
-                    taken[i] = n;
+                    if (TAKEN) taken[i] = n;
                     hi[i] = 0u;
                 }
             }
@@ -183,40 +182,42 @@ __device__ __forceinline__ int choose(const float (&l)[EPL], const float* bias, 
 }
 
 // K <= 64: a slot per lane.
-template <typename LT, int FMT, int EPL, bool BIAS>
+template <typename LT, int FMT, int EPL, bool BIAS, bool SIGMOID>
 __global__ __launch_bounds__(256) void k_gate(const LT* __restrict__ logits, int T, int E, int K,
-                                              const float* __restrict__ bias, int sigmoid, int normalize, float scale,
+                                              const float* __restrict__ bias, int normalize, float scale,
                                               void* __restrict__ routing, float* __restrict__ probs) {
     const int lane = threadIdx.x & 63;
     const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
+    const LT* row = logits + t * E;
     float l[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = lane + 64 * i < E ? load_logit(logits + t * E + lane + 64 * i) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) l[i] = lane + 64 * i < E ? load_logit(row + lane + 64 * i) : -INFINITY;
     double m = 0.0, sum = 1.0;
-    if (!sigmoid && (BIAS || !normalize)) softmax_terms<EPL>(l, &m, &sum);
+    if (!SIGMOID && (BIAS || !normalize)) softmax_terms<EPL>(l, &m, &sum);
     int my_e = -1, taken[EPL];
-    float my_l = -INFINITY;
-    const int n = choose<LT, EPL, BIAS>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken);
-    // weight of the lane's slot
-    double w = 0.0;
-    if (sigmoid) {
-        w = lane < n ? sigmoid_of((double)my_l) : 0.0;
+    const int n = choose<EPL, BIAS, SIGMOID, FMT == MOE_ROUTE_SPARSE_BOOL>(l, bias, E, K, m, sum, lane, &my_e, taken);
+    // weight of the lane's slot; its logit comes once more from the cache
+    const bool on = lane < n;
+    const double le = on ? (double)load_logit(row + my_e) : kOut;
+    double w;
+    if (SIGMOID) {
+        w = on ? sigmoid_of(le) : 0.0;
         if (normalize) {
             sum = wave_sum_dpp(w);
             if (sum < kTiny) {   // the same for every lane
-                const double ls = lane < n ? log_sigmoid((double)my_l) : kOut;
+                const double ls = on ? log_sigmoid(le) : kOut;
                 const double top = wave_max_dpp(ls);
-                w = lane < n ? exp(ls - top) : 0.0;
+                w = on ? exp(ls - top) : 0.0;
                 sum = wave_sum_dpp(w);
             }
         }
     } else {
-        if (normalize) m = wave_max_dpp((double)my_l);
-        w = lane < n ? exp_neg((double)my_l - m) : 0.0;
+        if (normalize) m = wave_max_dpp(le);
+        w = on ? exp_neg(le - m) : 0.0;
         if (normalize) sum = wave_sum_dpp(w);
     }
-    const float p = lane < n ? (float)(w * ((double)scale / sum)) : 0.f;
+    const float p = on ? (float)(w * ((double)scale / sum)) : 0.f;
     if constexpr (FMT == MOE_ROUTE_SPARSE_BOOL) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -249,9 +250,9 @@ __global__ __launch_bounds__(256) void k_gate_many(const LT* __restrict__ logits
     double m = 0.0, sum = 1.0;
     if (!sigmoid && (bias || !normalize)) softmax_terms<EPL>(l, &m, &sum);
     int my_e = -1, taken[EPL];
-    float my_l = -INFINITY;
-    const int n = bias ? choose<LT, EPL, true>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken)
-                       : choose<LT, EPL, false>(l, bias, E, K, sigmoid, m, sum, lane, &my_e, &my_l, taken);
+    const int n = !bias     ? choose<EPL, false, true, true>(l, bias, E, K, m, sum, lane, &my_e, taken)
+                  : sigmoid ? choose<EPL, true, true, true>(l, bias, E, K, m, sum, lane, &my_e, taken)
+                            : choose<EPL, true, false, true>(l, bias, E, K, m, sum, lane, &my_e, taken);
     double w[EPL], part = 0.0;
     if (normalize && !sigmoid) {
         m = kOut;
@@ -521,12 +522,16 @@ hipError_t launch_gate(const moe_handle* h, const void* logits, int logit_dtype,
             using LT = decltype(lt);
             constexpr int FMT = decltype(fmt)::value, EPL = decltype(epl)::value;
             auto go = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (const LT*)logits, d.T, d.E, d.K, bias, sigmoid,
-                                   normalize, scale, routing, probs);
+                hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (const LT*)logits, d.T, d.E, d.K, bias, normalize,
+                                   scale, routing, probs);
             };
-            if (d.K > 64) go(k_gate_many<LT, FMT, EPL>);
-            else if (bias) go(k_gate<LT, FMT, EPL, true>);
-            else go(k_gate<LT, FMT, EPL, false>);
+            if (d.K > 64)
+                hipLaunchKernelGGL((k_gate_many<LT, FMT, EPL>), grid, dim3(256), 0, s, (const LT*)logits, d.T, d.E,
+                                   d.K, bias, sigmoid, normalize, scale, routing, probs);
+            else if (bias && sigmoid) go(k_gate<LT, FMT, EPL, true, true>);
+            else if (bias) go(k_gate<LT, FMT, EPL, true, false>);
+            else if (sigmoid) go(k_gate<LT, FMT, EPL, false, true>);
+            else go(k_gate<LT, FMT, EPL, false, false>);
         });
     });
     return hipGetLastError();
