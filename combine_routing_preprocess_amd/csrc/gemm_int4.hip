@@ -9,9 +9,13 @@
 //
 //  * Work unit = (expert, 64 features) for FC1, (expert, 128 output rows) for
 //    FC2, one workgroup of four wavefronts per unit; a wavefront owns two
-//    16-row weight tiles (FC1: the gate and up rows of 16 features).  Whole
-//    128-byte lines (256 codes of a row) go through the wavefront's own LDS
-//    buffer into operand layout, as in the fp8 kernels.
+//    16-row weight tiles (FC1: the gate and up rows of 16 features).  Per step
+//    a unit takes one 128-byte line (256 codes) of every weight row, the
+//    line's scales (four steps' at a time) and the same 256 columns of its token rows, all straight
+//    from memory into an LDS ring (no registers, no write to LDS by the
+//    wavefronts); the weights and scales are the wavefront's own, the tokens
+//    are shared.  A step's data is loaded D - 1 steps ahead, so two workgroups
+//    per CU keep 64 KB in flight; one wait and one barrier per step.
 //  * Products on v_mfma_f32_16x16x32_bf16: token rows are the A operand
 //    (16 rows), weight rows the B operand (16 columns), so a lane dequantises
 //    and scales one weight row only.  A lane's 16-byte piece holds 32
@@ -26,7 +30,7 @@
 //  * After a group's MFMAs the fp32 block sum times the lane's scale is added
 //    to the accumulator: scales are never rounded.  Activations between FC1
 //    and FC2 are rounded once to bf16, as on the bf16 path.
-//  * Up to 4 token blocks (64 rows) per pass; more rows take more passes.
+//  * Up to 32 token rows per pass; more rows take more passes.
 #include "device_ops.h"
 
 namespace moe {
@@ -34,23 +38,73 @@ namespace {
 
 using namespace ops;
 
-typedef short bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2a __attribute__((ext_vector_type(2), aligned(4)));
-typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+constexpr int kCols = 256;            // columns of a step: a 128-byte line of codes, two scale groups
+constexpr int kWaveBytes = 32 * 128;  // codes of a wavefront's step
+constexpr int kUnitBytes = 4 * kWaveBytes;
+constexpr int kBlock = 4;             // steps that share a transfer of scales: 8 groups of 32 rows
+constexpr int kScaleBytes = 32 * 8 * 4;
+constexpr int kMaxRows = 32;          // token rows of a pass
 
-constexpr int kLine = 256;     // codes of a 128-byte line of a weight row: two scale groups
+// Steps in the ring for passes of up to `rows` token rows, and its bytes with
+// the two blocks of scales: at most half of the CU's 160 KB.
+constexpr int ring_depth(int rows) { return rows <= 16 ? 3 : 2; }
+constexpr int ring_bytes(int rows) { return ring_depth(rows) * (kUnitBytes + rows * kCols * 2); }
+constexpr int kScalesAt = ring_bytes(16) > ring_bytes(32) ? ring_bytes(16) : ring_bytes(32);
+constexpr int kRingBytes = kScalesAt + 2 * 4 * kScaleBytes;
+static_assert(2 * kRingBytes <= 160 * 1024, "two workgroups per CU");
+
+// Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
+// (wave-uniform) + voff (per lane) to LDS byte address lds + 16 * lane (4 *
+// lane).  Inline asm, so that the compiler does not wait for them before other
+// LDS reads; their completion is awaited explicitly.  m0 is written only here.
+typedef const char __attribute__((address_space(1))) gchar;
+__device__ __forceinline__ gchar* uniform_ptr(const void* p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (gchar*)(((uint64_t)hi << 32) | lo);
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void to_lds16(gchar* sbase, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds16_once(gchar* sbase, uint32_t voff, uint32_t lds) {   // data read once
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds4(gchar* sbase, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Workgroup barrier; this wavefront's LDS reads are complete before it
+// arrives, its transfers may be in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 __device__ __forceinline__ f32x4 mfma_bf16(const u32x4& a, const u32x4& b, const f32x4& c) {
     typedef __bf16 v8 __attribute__((ext_vector_type(8)));
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
 }
 
-// Eight codes -> eight bf16 16 + c, in column order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ u32x4 codes_bf16(uint32_t w) {
-    constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
-    return u32x4{((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
-                 ((w >> 9) & kMask) | kBase};
-}
+// Eight codes -> eight bf16 16 + c, in column order 0 4 1 5 2 6 3 7.  Mask and
+// base are held in registers the compiler knows nothing of: as constants they
+// would need two literals, and each and-or would become two instructions.
+struct CodeBits {
+    uint32_t mask = 0x00780078u, base = 0x41804180u;
+    __device__ __forceinline__ CodeBits() { asm("" : "+v"(mask), "+v"(base)); }
+    __device__ __forceinline__ u32x4 bf16(uint32_t w) const {
+        return u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base,
+                     ((w >> 9) & mask) | base};
+    }
+};
 
 // Eight consecutive bf16 into the same column order.
 __device__ __forceinline__ u32x4 pair_order(const u32x4& x) {
@@ -60,106 +114,160 @@ __device__ __forceinline__ u32x4 pair_order(const u32x4& x) {
 
 constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 of -24
 
-// One 128-column group: wq[i] = the lane's 16-byte piece of tile i's row
-// (columns 32 * (lane / 16) .. + 31 of the group), xg = the lane's token
-// columns at the same place, sc[i] = the scales of the lane's rows.
-template <int NTB>
-__device__ __forceinline__ void group_mac(const u32x4 (&wq)[2], const uint16_t* const (&xg)[NTB], const float (&sc)[2],
-                                          f32x4 (&acc)[2][NTB]) {
-    u32x4 b[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) b[i][q] = codes_bf16(wq[i][q]);
-    const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
-#pragma unroll
-    for (int t = 0; t < NTB; ++t) {
-        u32x4 a[4];
-        f32x4 z = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) a[q] = pair_order(*(const u32x4*)(xg[t] + 8 * q));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) z = mfma_bf16(a[q], off, z);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            f32x4 p = z;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) p = mfma_bf16(a[q], b[i][q], p);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][t][j] = fmaf(sc[i], p[j], acc[i][t][j]);
-        }
-    }
-}
-
-// K loop of one pass over rows m0 .. m0+mv-1 of the segment for the two
-// weight tiles at t0 / t1 (byte 0 of each tile's first row) with scales s0 /
-// s1 (the lane's own row).  On return lane l holds, for token m0 + 16 t + 4 *
-// (l / 16) + j, the sums of the tiles' rows l % 16 in acc[.][t][j].
-template <int NTB>
+// One pass over rows m0 .. m0+mv-1 of the segment (mv <= ROWS) for the two
+// weight tiles at t0 / t1 (byte 0 of each tile's first row) with scales at ws0
+// and, scale_step bytes further, for the second tile.  On return lane l holds,
+// for token 16 t + 4 * (l / 16) + j of the pass, the sums of the tiles' rows l
+// % 16 in acc[.][t][j].
+template <int ROWS>
 __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
-                                                const float* s0, const float* s1, long long seg, int m0, int mv,
-                                                int Kdim, int lane, unsigned char* lds, f32x4 (&acc)[2][NTB]) {
-    const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2;
+                                                const float* ws0, uint32_t scale_step, long long row0, int mv,
+                                                int Kdim, int lane, int wave, unsigned char* lds,
+                                                f32x4 (&acc)[2][(ROWS + 15) / 16]) {
+    constexpr int D = ring_depth(ROWS), NTB = (ROWS + 15) / 16, TL = ROWS / 8;
+    constexpr int kStage = kUnitBytes + ROWS * kCols * 2;
+    constexpr int kLoads = 4 + TL;         // transfers of a wavefront per step, but for the scales
+    const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2, groups = Kdim / 128;
+    const int steps = (Kdim + kCols - 1) / kCols;
+    const bool half_last = Kdim % kCols != 0;   // the last step holds one group only
 #pragma unroll
     for (int t = 0; t < NTB; ++t) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // the lane's token row in block t (clamped), at its 32 columns of a group
-    const uint16_t* xr[NTB];
-#pragma unroll
-    for (int t = 0; t < NTB; ++t) xr[t] = X + (size_t)(seg + m0 + min(16 * t + r16, mv - 1)) * Kdim + 32 * c1;
 
-    auto lines = [&](int kb0, auto uc) {   // UU whole lines of every row, all loads first
-        constexpr int UU = decltype(uc)::value;
-        u32x4 raw[UU][4];
-        wl_load<UU>(t0, t1, row_bytes, kb0, lane, raw);
-        wl_stash<UU>(lds, lane, raw);
+    // Sources.  16-byte pieces are swizzled on the way (the LDS side of a
+    // transfer is linear): piece p of weight row r lands in slot p ^ (r % 8) of
+    // its 8, piece p of token row r in slot p ^ (r % 16) of its 32.
+    const int wrow = lane >> 3, wpiece = (lane & 7) ^ wrow;
+    const uint32_t woff = (uint32_t)(wrow * row_bytes + 16 * wpiece);
+    const uint32_t woff_last = (uint32_t)(wrow * row_bytes + 16 * (half_last ? wpiece & 3 : wpiece));
+    // Scales of a block lie as [32 rows][8 groups].  Rows of whole 16-byte pieces take one transfer (row lane / 2,
+    // four groups), others four (row 8 i + lane / 8, one group); groups past the row's end repeat its last ones.
+    const bool wide = groups % 4 == 0;
+    auto scale_off = [&](int row, int g) {
+        return (uint32_t)(((row & 15) * groups + g) * 4) + (row & 16 ? scale_step : 0u);
+    };
+    uint32_t xoff[TL], xoff_last[TL];
 #pragma unroll
-        for (int u = 0; u < UU; ++u) {
-            const unsigned char* buf = lds + u * 4096;
-            const f32x2a sa = *(const f32x2a*)(s0 + 2 * (kb0 + u)), sb = *(const f32x2a*)(s1 + 2 * (kb0 + u));
+    for (int j = 0; j < TL; ++j) {
+        const int r = 2 * (wave + 4 * j) + (lane >> 5), p = (lane & 31) ^ (r & 15);
+        const uint32_t at = (uint32_t)min(r, mv - 1) * (uint32_t)Kdim * 2u;
+        xoff[j] = at + 16u * (uint32_t)p;
+        xoff_last[j] = at + 16u * (uint32_t)(half_last ? p & 15 : p);
+    }
+    gchar *b0 = uniform_ptr(t0), *b1 = uniform_ptr(t1), *bs = uniform_ptr(ws0);
+    gchar* bx = uniform_ptr(X + (size_t)row0 * Kdim);
+    const uint32_t ring = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
+    auto load_scales = [&](int blk) {
+        const uint32_t at = ring + kScalesAt + (uint32_t)((blk & 1) * 4 + wave) * kScaleBytes;
+        if (wide) {
+            to_lds16(bs, scale_off(lane >> 1, min(8 * blk + 4 * (lane & 1), groups - 4)), at);
+        } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int ch = c1 + 4 * half;
-                const u32x4 wq[2] = {*(const u32x4*)(buf + r16 * 128 + 16 * (ch ^ (r16 & 7))),
-                                     *(const u32x4*)(buf + (16 + r16) * 128 + 16 * (ch ^ (r16 & 7)))};
-                const float sc[2] = {sa[half], sb[half]};
-                const uint16_t* xg[NTB];
+            for (int i = 0; i < 4; ++i)
+                to_lds4(bs, scale_off(8 * i + (lane >> 3), min(8 * blk + (lane & 7), groups - 1)), at + 256 * i);
+        }
+    };
+    auto load = [&](int k) {
+        if (k % kBlock == 0) load_scales(k / kBlock);
+        const bool last = k == steps - 1;
+        const uint32_t at = ring + (uint32_t)(k % D) * kStage;
+        const uint32_t aw = at + (uint32_t)wave * kWaveBytes;
+        const size_t line = (size_t)k * 128;
+        const uint32_t wo = last ? woff_last : woff;
+        to_lds16_once(b0 + line, wo, aw);
+        to_lds16_once(b0 + line + 8 * (size_t)row_bytes, wo, aw + 1024);
+        to_lds16_once(b1 + line, wo, aw + 2048);
+        to_lds16_once(b1 + line + 8 * (size_t)row_bytes, wo, aw + 3072);
 #pragma unroll
-                for (int t = 0; t < NTB; ++t) xg[t] = xr[t] + (size_t)(kb0 + u) * kLine + 128 * half;
-                group_mac<NTB>(wq, xg, sc, acc);
+        for (int j = 0; j < TL; ++j)
+            to_lds16(bx + (size_t)k * (kCols * 2), last ? xoff_last[j] : xoff[j],
+                     at + kUnitBytes + (uint32_t)(wave + 4 * j) * 1024);
+    };
+    const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
+    const CodeBits bits;
+    auto group = [&](int k, int slot, int half) {
+        const unsigned char* st = lds + slot * kStage;
+        const unsigned char* sw = st + wave * kWaveBytes;
+        const float* ss = (const float*)(lds + kScalesAt + ((k / kBlock & 1) * 4 + wave) * kScaleBytes) +
+                          2 * (k % kBlock) + half;
+        u32x4 b[2][4];
+        float sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const u32x4 wq = *(const u32x4*)(sw + (16 * i + r16) * 128 + 16 * ((c1 + 4 * half) ^ (r16 & 7)));
+            sc[i] = ss[8 * (16 * i + r16)];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[i][q] = bits.bf16(wq[q]);
+        }
+#pragma unroll
+        for (int t = 0; t < NTB; ++t) {
+            const int r = 16 * t + (ROWS < 16 ? r16 % ROWS : r16);
+            u32x4 a[4];
+            f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                a[q] = pair_order(*(const u32x4*)(st + kUnitBytes + r * (kCols * 2) +
+                                                  16 * ((16 * half + 4 * c1 + q) ^ (r & 15))));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) z = mfma_bf16(a[q], off, z);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f32x4 p = z;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) p = mfma_bf16(a[q], b[i][q], p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][t][j] = fmaf(sc[i], p[j], acc[i][t][j]);
             }
         }
     };
-    const int nl = Kdim / kLine;
-    int kb = 0;
-    for (; kb + kU <= nl; kb += kU) lines(kb, std::integral_constant<int, kU>{});
-    for (; kb < nl; ++kb) lines(kb, std::integral_constant<int, 1>{});
-    if (Kdim % kLine) {   // an odd number of groups: the last one straight in operand layout
-        const size_t o = (size_t)r16 * row_bytes + (size_t)nl * 128 + 16 * c1;
-        const u32x4 wq[2] = {__builtin_nontemporal_load((const u32x4*)(t0 + o)),
-                             __builtin_nontemporal_load((const u32x4*)(t1 + o))};
-        const float sc[2] = {s0[2 * nl], s1[2 * nl]};
-        const uint16_t* xg[NTB];
+    wait_vm<0>();      // the counts below are of the transfers alone
+    lds_barrier();     // nobody reads the previous pass's ring any more
 #pragma unroll
-        for (int t = 0; t < NTB; ++t) xg[t] = xr[t] + (size_t)nl * kLine;
-        group_mac<NTB>(wq, xg, sc, acc);
+    for (int k = 0; k < D - 1; ++k)
+        if (k < steps) load(k);
+    auto arrive = [&](int k) {
+        // the transfers of step k have landed, those of the D - 2 steps after it may be in flight
+        if (D > 2 && k + 1 < steps) {
+            if (wide && (k + 1) % kBlock == 0) wait_vm<kLoads + 1>();
+            else wait_vm<kLoads>();
+        } else {
+            wait_vm<0>();
+        }
+        lds_barrier();
+        if (k + D - 1 < steps) load(k + D - 1);   // into the slot that step k - 1 was read from
+    };
+    static_assert(D <= 3, "arrive() lets one step be in flight");
+    const int whole = steps - (half_last ? 1 : 0);
+    for (int k0 = 0; k0 < whole; k0 += D)
+#pragma unroll
+        for (int u = 0; u < D; ++u)   // the slot of step k0 + u is u: a constant in every LDS address
+            if (k0 + u < whole) {
+                arrive(k0 + u);
+                group(k0 + u, u, 0);
+                group(k0 + u, u, 1);
+            }
+    if (half_last) {
+        arrive(whole);
+        group(whole, whole % D, 0);
     }
 }
 
 // MODE 0: SwiGLU of (gate, up) at feature f0 + l % 16; MODE 1: output rows
 // f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout].
-template <int MODE, int NTB>
+template <int MODE, int ROWS>
 __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
-                                          const float* s0, const float* s1, uint16_t* __restrict__ Out, long long seg,
-                                          int m0, int mv, int Kdim, int Nout, int f0, int lane, unsigned char* lds) {
-    f32x4 acc[2][NTB];
-    int4_accumulate<NTB>(X, t0, t1, s0, s1, seg, m0, mv, Kdim, lane, lds, acc);
+                                          const float* ws0, uint32_t scale_step, uint16_t* __restrict__ Out,
+                                          long long row0, int mv, int Kdim, int Nout, int f0, int lane, int wave,
+                                          unsigned char* lds) {
+    f32x4 acc[2][(ROWS + 15) / 16];
+    int4_accumulate<ROWS>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, lds, acc);
 #pragma unroll
-    for (int t = 0; t < NTB; ++t)
+    for (int t = 0; t < (ROWS + 15) / 16; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int tok = 16 * t + 4 * (lane >> 4) + j;
             if (tok >= mv) continue;
-            uint16_t* o = Out + (size_t)(seg + m0 + tok) * Nout + f0 + (lane & 15);
+            uint16_t* o = Out + (size_t)(row0 + tok) * Nout + f0 + (lane & 15);
             if (MODE == 0) {
                 o[0] = (uint16_t)f32_to_bf16(swiglu(acc[0][t][j], acc[1][t][j]));
             } else {
@@ -169,34 +277,38 @@ __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const 
         }
 }
 
+// blockIdx.y: passes y, y + gridDim.y, ... of the expert's rows, `rows` token
+// rows each.
+// At least two wavefronts per SIMD: 256 registers, and matrix results in vector registers.
 template <int MODE>
-__global__ __launch_bounds__(256) void k_gemm_int4(const uint16_t* __restrict__ X, const uint8_t* __restrict__ W,
+__global__ __launch_bounds__(256, 2) void k_gemm_int4(const uint16_t* __restrict__ X, const uint8_t* __restrict__ W,
                                                    const float* __restrict__ Ws, uint16_t* __restrict__ Out,
                                                    const int64_t* __restrict__ seg_off,
                                                    const int32_t* __restrict__ kept, long long R, int Kdim, int Wrows,
-                                                   int Nout, int units_per_expert) {
-    __shared__ __attribute__((aligned(16))) unsigned char s_w[4 * kWaveLds];
+                                                   int Nout, int units_per_expert, int rows) {
+    __shared__ __attribute__((aligned(16))) unsigned char s_ring[kRingBytes];
     const int e = blockIdx.x / units_per_expert;
     const int unit = blockIdx.x - e * units_per_expert;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long long seg = seg_off[e];
     long long me_l = seg < R ? (long long)kept[e] : 0;
     if (seg + me_l > R) me_l = R - seg;
     const int me = (int)me_l;
-    if (me <= 0) return;
     const int f0 = MODE == 0 ? unit * kFeat + wave * 16 : unit * kFeat2 + wave * 32;
-    const size_t r0 = (size_t)e * Wrows + f0, r1 = r0 + (MODE == 0 ? Nout : 16);
-    const uint8_t *t0 = W + r0 * (Kdim / 2), *t1 = W + r1 * (Kdim / 2);
-    const float *s0 = Ws + (r0 + (lane & 15)) * (Kdim / 128), *s1 = Ws + (r1 + (lane & 15)) * (Kdim / 128);
-    unsigned char* lds = s_w + wave * kWaveLds;
-    for (int m0 = 0; m0 < me; m0 += 16 * kMaxTB) {
-        const int mv = min(16 * kMaxTB, me - m0);
-        switch ((mv + 15) / 16) {
-            case 1: int4_pass<MODE, 1>(X, t0, t1, s0, s1, Out, seg, m0, mv, Kdim, Nout, f0, lane, lds); break;
-            case 2: int4_pass<MODE, 2>(X, t0, t1, s0, s1, Out, seg, m0, mv, Kdim, Nout, f0, lane, lds); break;
-            case 3: int4_pass<MODE, 3>(X, t0, t1, s0, s1, Out, seg, m0, mv, Kdim, Nout, f0, lane, lds); break;
-            default: int4_pass<MODE, 4>(X, t0, t1, s0, s1, Out, seg, m0, mv, Kdim, Nout, f0, lane, lds); break;
-        }
+    const size_t r0 = (size_t)e * Wrows + f0, step = MODE == 0 ? Nout : 16;
+    const uint8_t *t0 = W + r0 * (Kdim / 2), *t1 = t0 + step * (Kdim / 2);
+    const float* ws0 = Ws + r0 * (Kdim / 128);
+    const uint32_t scale_step = (uint32_t)(step * (Kdim / 128) * 4);
+    for (int m0 = blockIdx.y * rows; m0 < me; m0 += gridDim.y * rows) {
+        const int mv = min(rows, me - m0);
+        const long long row0 = seg + m0;
+        auto pass = [&](auto n) {
+            int4_pass<MODE, decltype(n)::value>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0, lane, wave,
+                                                s_ring);
+        };
+        if (mv <= 8) pass(std::integral_constant<int, 8>{});
+        else if (mv <= 16) pass(std::integral_constant<int, 16>{});
+        else pass(std::integral_constant<int, 32>{});
     }
 }
 
@@ -207,15 +319,15 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     const moe_desc& d = h->desc;
     const long long R = d.out_rows;
     if (R == 0) return hipSuccess;
-    if (stage == 0) {
-        const int upe = F / kFeat;
-        hipLaunchKernelGGL(k_gemm_int4<0>, dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w,
-                           ws, (uint16_t*)out, h->seg_off, h->kept, R, d.H, 2 * F, F, upe);
-    } else {
-        const int upe = d.H / kFeat2;
-        hipLaunchKernelGGL(k_gemm_int4<1>, dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w,
-                           ws, (uint16_t*)out, h->seg_off, h->kept, R, F, d.H, d.H, upe);
-    }
+    const int upe = stage == 0 ? F / kFeat : d.H / kFeat2;
+    const int rows = kMaxRows;
+    const dim3 grid((unsigned)(d.E * upe), 1u);
+    if (stage == 0)
+        hipLaunchKernelGGL(k_gemm_int4<0>, grid, dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w, ws,
+                           (uint16_t*)out, h->seg_off, h->kept, R, d.H, 2 * F, F, upe, rows);
+    else
+        hipLaunchKernelGGL(k_gemm_int4<1>, grid, dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w, ws,
+                           (uint16_t*)out, h->seg_off, h->kept, R, F, d.H, d.H, upe, rows);
     return hipGetLastError();
 }
 
