@@ -41,17 +41,17 @@ using namespace ops;
 constexpr int kCols = 256;            // columns of a step: a 128-byte line of codes, two scale groups
 constexpr int kWaveBytes = 32 * 128;  // codes of a wavefront's step
 constexpr int kUnitBytes = 4 * kWaveBytes;
-constexpr int kBlock = 4;             // steps that share a transfer of scales: 8 groups of 32 rows
-constexpr int kScaleBytes = 32 * 8 * 4;
-constexpr int kMaxRows = 32;          // token rows of a pass
+constexpr int kBlock = 2;             // steps that share a transfer of scales: 4 groups of 32 rows
+constexpr int kScaleBytes = 32 * 4 * 4;
+constexpr int kDepth = 2;             // steps in the ring
 
-// Steps in the ring for passes of up to `rows` token rows, and its bytes with
-// the two blocks of scales: at most half of the CU's 160 KB.
-constexpr int ring_depth(int rows) { return rows <= 16 ? 3 : 2; }
-constexpr int ring_bytes(int rows) { return ring_depth(rows) * (kUnitBytes + rows * kCols * 2); }
-constexpr int kScalesAt = ring_bytes(16) > ring_bytes(32) ? ring_bytes(16) : ring_bytes(32);
-constexpr int kRingBytes = kScalesAt + 2 * 4 * kScaleBytes;
-static_assert(2 * kRingBytes <= 160 * 1024, "two workgroups per CU");
+// LDS of a kernel for passes of up to `rows` token rows: the ring, and two
+// blocks of scales per wavefront.
+constexpr int kScaleRing = 2 * 4 * kScaleBytes;
+constexpr int lds_bytes(int rows) { return kScaleRing + kDepth * (kUnitBytes + rows * kCols * 2); }
+// Workgroups per CU that fit its 160 KB.
+constexpr int per_cu(int rows) { return 160 * 1024 / lds_bytes(rows); }
+static_assert(per_cu(16) == 3 && per_cu(32) == 2, "LDS budget");
 
 // Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
 // (wave-uniform) + voff (per lane) to LDS byte address lds + 16 * lane (4 *
@@ -124,9 +124,8 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
                                                 int Kdim, int lane, int wave, unsigned char* lds,
                                                 f32x4 (&acc)[2][(ROWS + 15) / 16]) {
-    constexpr int D = ring_depth(ROWS), NTB = (ROWS + 15) / 16, TL = ROWS / 8;
+    constexpr int D = kDepth, NTB = (ROWS + 15) / 16, TL = ROWS / 8;
     constexpr int kStage = kUnitBytes + ROWS * kCols * 2;
-    constexpr int kLoads = 4 + TL;         // transfers of a wavefront per step, but for the scales
     const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2, groups = Kdim / 128;
     const int steps = (Kdim + kCols - 1) / kCols;
     const bool half_last = Kdim % kCols != 0;   // the last step holds one group only
@@ -139,8 +138,8 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     const int wrow = lane >> 3, wpiece = (lane & 7) ^ wrow;
     const uint32_t woff = (uint32_t)(wrow * row_bytes + 16 * wpiece);
     const uint32_t woff_last = (uint32_t)(wrow * row_bytes + 16 * (half_last ? wpiece & 3 : wpiece));
-    // Scales of a block lie as [32 rows][8 groups].  Rows of whole 16-byte pieces take one transfer (row lane / 2,
-    // four groups), others four (row 8 i + lane / 8, one group); groups past the row's end repeat its last ones.
+    // Scales of a block lie as [32 rows][4 groups].  Rows of whole 16-byte pieces take one transfer (row lane of
+    // the lower 32 lanes), others two (row 16 i + lane / 4, one group); groups past the row's end repeat its last.
     const bool wide = groups % 4 == 0;
     auto scale_off = [&](int row, int g) {
         return (uint32_t)(((row & 15) * groups + g) * 4) + (row & 16 ? scale_step : 0u);
@@ -158,19 +157,19 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     const uint32_t ring = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
     auto load_scales = [&](int blk) {
-        const uint32_t at = ring + kScalesAt + (uint32_t)((blk & 1) * 4 + wave) * kScaleBytes;
+        const uint32_t at = ring + (uint32_t)((blk & 1) * 4 + wave) * kScaleBytes;
         if (wide) {
-            to_lds16(bs, scale_off(lane >> 1, min(8 * blk + 4 * (lane & 1), groups - 4)), at);
+            if (lane < 32) to_lds16(bs, scale_off(lane, 4 * blk), at);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to_lds4(bs, scale_off(8 * i + (lane >> 3), min(8 * blk + (lane & 7), groups - 1)), at + 256 * i);
+            for (int i = 0; i < 2; ++i)
+                to_lds4(bs, scale_off(16 * i + (lane >> 2), min(4 * blk + (lane & 3), groups - 1)), at + 256 * i);
         }
     };
     auto load = [&](int k) {
         if (k % kBlock == 0) load_scales(k / kBlock);
         const bool last = k == steps - 1;
-        const uint32_t at = ring + (uint32_t)(k % D) * kStage;
+        const uint32_t at = ring + kScaleRing + (uint32_t)(k % D) * kStage;
         const uint32_t aw = at + (uint32_t)wave * kWaveBytes;
         const size_t line = (size_t)k * 128;
         const uint32_t wo = last ? woff_last : woff;
@@ -186,16 +185,15 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
     const CodeBits bits;
     auto group = [&](int k, int slot, int half) {
-        const unsigned char* st = lds + slot * kStage;
+        const unsigned char* st = lds + kScaleRing + slot * kStage;
         const unsigned char* sw = st + wave * kWaveBytes;
-        const float* ss = (const float*)(lds + kScalesAt + ((k / kBlock & 1) * 4 + wave) * kScaleBytes) +
-                          2 * (k % kBlock) + half;
+        const float* ss = (const float*)(lds + ((k / kBlock & 1) * 4 + wave) * kScaleBytes) + 2 * (k % kBlock) + half;
         u32x4 b[2][4];
         float sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const u32x4 wq = *(const u32x4*)(sw + (16 * i + r16) * 128 + 16 * ((c1 + 4 * half) ^ (r16 & 7)));
-            sc[i] = ss[8 * (16 * i + r16)];
+            sc[i] = ss[4 * (16 * i + r16)];
 #pragma unroll
             for (int q = 0; q < 4; ++q) b[i][q] = bits.bf16(wq[q]);
         }
@@ -220,27 +218,17 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
             }
         }
     };
-    wait_vm<0>();      // the counts below are of the transfers alone
     lds_barrier();     // nobody reads the previous pass's ring any more
-#pragma unroll
-    for (int k = 0; k < D - 1; ++k)
-        if (k < steps) load(k);
+    load(0);
     auto arrive = [&](int k) {
-        // the transfers of step k have landed, those of the D - 2 steps after it may be in flight
-        if (D > 2 && k + 1 < steps) {
-            if (wide && (k + 1) % kBlock == 0) wait_vm<kLoads + 1>();
-            else wait_vm<kLoads>();
-        } else {
-            wait_vm<0>();
-        }
+        wait_vm<0>();      // step k has landed
         lds_barrier();
-        if (k + D - 1 < steps) load(k + D - 1);   // into the slot that step k - 1 was read from
+        if (k + 1 < steps) load(k + 1);   // into the slot that step k - 1 was read from
     };
-    static_assert(D <= 3, "arrive() lets one step be in flight");
     const int whole = steps - (half_last ? 1 : 0);
     for (int k0 = 0; k0 < whole; k0 += D)
 #pragma unroll
-        for (int u = 0; u < D; ++u)   // the slot of step k0 + u is u: a constant in every LDS address
+        for (int u = 0; u < D; ++u)   // step k0 + u is in slot u: a constant in every LDS address
             if (k0 + u < whole) {
                 arrive(k0 + u);
                 group(k0 + u, u, 0);
@@ -277,16 +265,14 @@ __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const 
         }
 }
 
-// blockIdx.y: passes y, y + gridDim.y, ... of the expert's rows, `rows` token
-// rows each.
-// At least two wavefronts per SIMD: 256 registers, and matrix results in vector registers.
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void k_gemm_int4(const uint16_t* __restrict__ X, const uint8_t* __restrict__ W,
-                                                   const float* __restrict__ Ws, uint16_t* __restrict__ Out,
-                                                   const int64_t* __restrict__ seg_off,
-                                                   const int32_t* __restrict__ kept, long long R, int Kdim, int Wrows,
-                                                   int Nout, int units_per_expert, int rows) {
-    __shared__ __attribute__((aligned(16))) unsigned char s_ring[kRingBytes];
+// Passes of up to ROWS token rows each.  At least per_cu(ROWS) wavefronts per
+// SIMD, which also keeps matrix results in vector registers.
+template <int MODE, int ROWS>
+__global__ __launch_bounds__(256, per_cu(ROWS)) void k_gemm_int4(
+    const uint16_t* __restrict__ X, const uint8_t* __restrict__ W, const float* __restrict__ Ws,
+    uint16_t* __restrict__ Out, const int64_t* __restrict__ seg_off, const int32_t* __restrict__ kept, long long R,
+    int Kdim, int Wrows, int Nout, int units_per_expert) {
+    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS)];
     const int e = blockIdx.x / units_per_expert;
     const int unit = blockIdx.x - e * units_per_expert;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -299,16 +285,16 @@ __global__ __launch_bounds__(256, 2) void k_gemm_int4(const uint16_t* __restrict
     const uint8_t *t0 = W + r0 * (Kdim / 2), *t1 = t0 + step * (Kdim / 2);
     const float* ws0 = Ws + r0 * (Kdim / 128);
     const uint32_t scale_step = (uint32_t)(step * (Kdim / 128) * 4);
-    for (int m0 = blockIdx.y * rows; m0 < me; m0 += gridDim.y * rows) {
-        const int mv = min(rows, me - m0);
+    for (int m0 = 0; m0 < me; m0 += ROWS) {
+        const int mv = min(ROWS, me - m0);
         const long long row0 = seg + m0;
         auto pass = [&](auto n) {
             int4_pass<MODE, decltype(n)::value>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0, lane, wave,
                                                 s_ring);
         };
         if (mv <= 8) pass(std::integral_constant<int, 8>{});
-        else if (mv <= 16) pass(std::integral_constant<int, 16>{});
-        else pass(std::integral_constant<int, 32>{});
+        else if (ROWS == 16 || mv <= 16) pass(std::integral_constant<int, 16>{});
+        else pass(std::integral_constant<int, ROWS>{});
     }
 }
 
@@ -320,14 +306,17 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     const long long R = d.out_rows;
     if (R == 0) return hipSuccess;
     const int upe = stage == 0 ? F / kFeat : d.H / kFeat2;
-    const int rows = kMaxRows;
-    const dim3 grid((unsigned)(d.E * upe), 1u);
-    if (stage == 0)
-        hipLaunchKernelGGL(k_gemm_int4<0>, grid, dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w, ws,
-                           (uint16_t*)out, h->seg_off, h->kept, R, d.H, 2 * F, F, upe, rows);
-    else
-        hipLaunchKernelGGL(k_gemm_int4<1>, grid, dim3(256), 0, s, (const uint16_t*)in, (const uint8_t*)w, ws,
-                           (uint16_t*)out, h->seg_off, h->kept, R, F, d.H, d.H, upe, rows);
+    auto go = [&](auto rows) {
+        constexpr int ROWS = decltype(rows)::value;
+        if (stage == 0)
+            hipLaunchKernelGGL((k_gemm_int4<0, ROWS>), dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.H, 2 * F, F, upe);
+        else
+            hipLaunchKernelGGL((k_gemm_int4<1, ROWS>), dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, F, d.H, d.H, upe);
+    };
+    if ((long long)d.T * d.K <= 8ll * d.E) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 32>{});
     return hipGetLastError();
 }
 
