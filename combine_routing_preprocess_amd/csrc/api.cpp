@@ -333,7 +333,7 @@ int moe_grouped_fc1_swiglu(const moe_handle* h, int32_t F, int32_t wdtype, const
         return hip_rc(launch_gemm_fp8(h, 0, F, d_perm, d_perm_scales, d_w1, d_w1_scales, d_scratch, nullptr,
                                       (hipStream_t)stream));
     if (wdtype == MOE_INT4_G128)
-        return hip_rc(launch_gemm_int4(h, 0, F, d_perm, d_w1, d_w1_scales, d_scratch, (hipStream_t)stream));
+        return hip_rc(launch_gemm_int4(h, 0, F, d_perm, d_w1, d_w1_scales, d_scratch, ncu, (hipStream_t)stream));
     return hip_rc(launch_gemm_bf16(h, 0, F, d_perm, d_w1, d_scratch, nullptr, ncu, (hipStream_t)stream));
 }
 
@@ -349,7 +349,7 @@ int moe_grouped_fc2(const moe_handle* h, int32_t F, int32_t wdtype, const void* 
         return hip_rc(launch_gemm_fp8(h, 1, F, nullptr, nullptr, d_w2, d_w2_scales, d_scratch, d_expert_out,
                                       (hipStream_t)stream));
     if (wdtype == MOE_INT4_G128)
-        return hip_rc(launch_gemm_int4(h, 1, F, d_scratch, d_w2, d_w2_scales, d_expert_out, (hipStream_t)stream));
+        return hip_rc(launch_gemm_int4(h, 1, F, d_scratch, d_w2, d_w2_scales, d_expert_out, ncu, (hipStream_t)stream));
     return hip_rc(launch_gemm_bf16(h, 1, F, d_scratch, d_w2, d_expert_out, nullptr, ncu, (hipStream_t)stream));
 }
 

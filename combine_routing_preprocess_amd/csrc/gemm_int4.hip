@@ -43,15 +43,17 @@ constexpr int kWaveBytes = 32 * 128;  // codes of a wavefront's step
 constexpr int kUnitBytes = 4 * kWaveBytes;
 constexpr int kBlock = 2;             // steps that share a transfer of scales: 4 groups of 32 rows
 constexpr int kScaleBytes = 32 * 4 * 4;
-constexpr int kDepth = 2;             // steps in the ring
 
-// LDS of a kernel for passes of up to `rows` token rows: the ring, and two
-// blocks of scales per wavefront.
-constexpr int kScaleRing = 2 * 4 * kScaleBytes;
-constexpr int lds_bytes(int rows) { return kScaleRing + kDepth * (kUnitBytes + rows * kCols * 2); }
+// LDS of a kernel for passes of up to `rows` token rows with `depth` steps in
+// the ring: the ring, and two blocks of scales per wavefront (more in a deeper
+// ring: a block is read until depth - 1 steps after the next one's transfer).
+constexpr int scale_blocks(int depth) { return (depth + kBlock - 1) / kBlock + 1; }
+constexpr int lds_bytes(int rows, int depth) {
+    return scale_blocks(depth) * 4 * kScaleBytes + depth * (kUnitBytes + rows * kCols * 2);
+}
 // Workgroups per CU that fit its 160 KB.
-constexpr int per_cu(int rows) { return 160 * 1024 / lds_bytes(rows); }
-static_assert(per_cu(16) == 3 && per_cu(32) == 2, "LDS budget");
+constexpr int per_cu(int rows, int depth) { return 160 * 1024 / lds_bytes(rows, depth); }
+static_assert(per_cu(16, 2) == 3 && per_cu(16, 3) == 2 && per_cu(16, 6) == 1 && per_cu(32, 2) == 2, "LDS budget");
 
 // Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
 // (wave-uniform) + voff (per lane) to LDS byte address lds + 16 * lane (4 *
@@ -119,12 +121,13 @@ constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 of -24
 // and, scale_step bytes further, for the second tile.  On return lane l holds,
 // for token 16 t + 4 * (l / 16) + j of the pass, the sums of the tiles' rows l
 // % 16 in acc[.][t][j].
-template <int ROWS>
+template <int ROWS, int D>
 __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
                                                 int Kdim, int lane, int wave, unsigned char* lds,
                                                 f32x4 (&acc)[2][(ROWS + 15) / 16]) {
-    constexpr int D = kDepth, NTB = (ROWS + 15) / 16, TL = ROWS / 8;
+    constexpr int NTB = (ROWS + 15) / 16, TL = ROWS / 8, SB = scale_blocks(D), kScaleRing = SB * 4 * kScaleBytes;
+    constexpr int kLoads = 4 + TL;         // transfers of a wavefront per step, but for the scales
     constexpr int kStage = kUnitBytes + ROWS * kCols * 2;
     const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2, groups = Kdim / 128;
     const int steps = (Kdim + kCols - 1) / kCols;
@@ -157,7 +160,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     const uint32_t ring = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
     auto load_scales = [&](int blk) {
-        const uint32_t at = ring + (uint32_t)((blk & 1) * 4 + wave) * kScaleBytes;
+        const uint32_t at = ring + (uint32_t)(blk % SB * 4 + wave) * kScaleBytes;
         if (wide) {
             if (lane < 32) to_lds16(bs, scale_off(lane, 4 * blk), at);
         } else {
@@ -187,7 +190,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     auto group = [&](int k, int slot, int half) {
         const unsigned char* st = lds + kScaleRing + slot * kStage;
         const unsigned char* sw = st + wave * kWaveBytes;
-        const float* ss = (const float*)(lds + ((k / kBlock & 1) * 4 + wave) * kScaleBytes) + 2 * (k % kBlock) + half;
+        const float* ss = (const float*)(lds + (k / kBlock % SB * 4 + wave) * kScaleBytes) + 2 * (k % kBlock) + half;
         u32x4 b[2][4];
         float sc[2];
 #pragma unroll
@@ -218,12 +221,22 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
             }
         }
     };
+    wait_vm<0>();      // the counts below are of the transfers alone
     lds_barrier();     // nobody reads the previous pass's ring any more
-    load(0);
+#pragma unroll
+    for (int k = 0; k < D - 1; ++k)
+        if (k < steps) load(k);
     auto arrive = [&](int k) {
-        wait_vm<0>();      // step k has landed
+        // Step k has landed; the transfers of up to D - 2 steps after it may be in flight.  They complete in order,
+        // and counting the scales' among the steps' only waits for a little more.
+        const int later = min(D - 2, steps - 1 - k);
+        if (later >= 4) wait_vm<4 * kLoads>();
+        else if (later == 3) wait_vm<3 * kLoads>();
+        else if (later == 2) wait_vm<2 * kLoads>();
+        else if (later == 1) wait_vm<kLoads>();
+        else wait_vm<0>();
         lds_barrier();
-        if (k + 1 < steps) load(k + 1);   // into the slot that step k - 1 was read from
+        if (k + D - 1 < steps) load(k + D - 1);   // into the slot that step k - 1 was read from
     };
     const int whole = steps - (half_last ? 1 : 0);
     for (int k0 = 0; k0 < whole; k0 += D)
@@ -242,13 +255,13 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
 
 // MODE 0: SwiGLU of (gate, up) at feature f0 + l % 16; MODE 1: output rows
 // f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout].
-template <int MODE, int ROWS>
+template <int MODE, int ROWS, int D>
 __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                           const float* ws0, uint32_t scale_step, uint16_t* __restrict__ Out,
                                           long long row0, int mv, int Kdim, int Nout, int f0, int lane, int wave,
                                           unsigned char* lds) {
     f32x4 acc[2][(ROWS + 15) / 16];
-    int4_accumulate<ROWS>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, lds, acc);
+    int4_accumulate<ROWS, D>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, lds, acc);
 #pragma unroll
     for (int t = 0; t < (ROWS + 15) / 16; ++t)
 #pragma unroll
@@ -265,17 +278,46 @@ __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const 
         }
 }
 
-// Passes of up to ROWS token rows each.  At least per_cu(ROWS) wavefronts per
-// SIMD, which also keeps matrix results in vector registers.
-template <int MODE, int ROWS>
-__global__ __launch_bounds__(256, per_cu(ROWS)) void k_gemm_int4(
+// The n-th expert that has rows, -1 if there are not as many; the same in every
+// wavefront.
+__device__ __forceinline__ int nth_with_rows(const int32_t* __restrict__ kept, int E, int n, int lane) {
+    for (int e0 = 0; e0 < E; e0 += 256) {
+        bool has[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + 64 * i + lane;
+            has[i] = e < E && kept[min(e, E - 1)] > 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t mask = __ballot(has[i]);
+            const int c = __popcll(mask);
+            if (n < c) {
+                const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                return e0 + 64 * i + __ffsll((unsigned long long)__ballot(has[i] && rank == n)) - 1;
+            }
+            n -= c;
+        }
+    }
+    return -1;
+}
+
+// Passes of up to ROWS token rows each: pass blockIdx.y and every gridDim.y-th
+// after it.  `sparse`: blockIdx.x counts the units of the experts that have
+// rows, otherwise of all.  At least per_cu wavefronts per SIMD, two of them to
+// keep matrix results in vector registers.
+template <int MODE, int ROWS, int D>
+__global__ __launch_bounds__(256, per_cu(ROWS, D) > 2 ? per_cu(ROWS, D) : 2) void k_gemm_int4(
     const uint16_t* __restrict__ X, const uint8_t* __restrict__ W, const float* __restrict__ Ws,
     uint16_t* __restrict__ Out, const int64_t* __restrict__ seg_off, const int32_t* __restrict__ kept, long long R,
-    int Kdim, int Wrows, int Nout, int units_per_expert) {
-    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS)];
-    const int e = blockIdx.x / units_per_expert;
-    const int unit = blockIdx.x - e * units_per_expert;
+    int E, int Kdim, int Wrows, int Nout, int units_per_expert, int sparse) {
+    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS, D)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int e = blockIdx.x / units_per_expert;
+    const int unit = blockIdx.x - e * units_per_expert;
+    if (sparse) e = nth_with_rows(kept, E, e, lane);
+    if (e < 0) return;
     const long long seg = seg_off[e];
     long long me_l = seg < R ? (long long)kept[e] : 0;
     if (seg + me_l > R) me_l = R - seg;
@@ -285,11 +327,11 @@ __global__ __launch_bounds__(256, per_cu(ROWS)) void k_gemm_int4(
     const uint8_t *t0 = W + r0 * (Kdim / 2), *t1 = t0 + step * (Kdim / 2);
     const float* ws0 = Ws + r0 * (Kdim / 128);
     const uint32_t scale_step = (uint32_t)(step * (Kdim / 128) * 4);
-    for (int m0 = 0; m0 < me; m0 += ROWS) {
+    for (int m0 = blockIdx.y * ROWS; m0 < me; m0 += gridDim.y * ROWS) {
         const int mv = min(ROWS, me - m0);
         const long long row0 = seg + m0;
         auto pass = [&](auto n) {
-            int4_pass<MODE, decltype(n)::value>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0, lane, wave,
+            int4_pass<MODE, decltype(n)::value, D>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0, lane, wave,
                                                 s_ring);
         };
         if (mv <= 8) pass(std::integral_constant<int, 8>{});
@@ -301,22 +343,36 @@ __global__ __launch_bounds__(256, per_cu(ROWS)) void k_gemm_int4(
 }  // namespace
 
 hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* in, const void* w, const float* ws,
-                            void* out, hipStream_t s) {
+                            void* out, int num_cu, hipStream_t s) {
     const moe_desc& d = h->desc;
-    const long long R = d.out_rows;
-    if (R == 0) return hipSuccess;
+    const long long R = d.out_rows, copies = (long long)d.T * d.K;
+    if (R == 0 || copies == 0) return hipSuccess;
     const int upe = stage == 0 ? F / kFeat : d.H / kFeat2;
-    auto go = [&](auto rows) {
-        constexpr int ROWS = decltype(rows)::value;
+    // experts that can have rows, and units to run; fewer copies than experts: skip the experts without rows by
+    // counting (their empty workgroups would hold the CUs' LDS in turns: one token took 50 us in FC1 with them)
+    const bool sparse = copies < d.E;
+    const int experts = sparse ? (int)copies : d.E;
+    const long long units = (long long)experts * upe;
+    const long long avg = (copies + experts - 1) / experts;   // rows per expert, if they are spread evenly
+    auto go = [&](auto rows, auto depth) {
+        constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value;
+        // passes of their own workgroups while the units alone leave CUs idle
+        const long long fill = (2ll * num_cu + units - 1) / units, passes = (avg + ROWS - 1) / ROWS;
+        const dim3 grid((unsigned)units, (unsigned)(fill < passes ? fill : passes));
         if (stage == 0)
-            hipLaunchKernelGGL((k_gemm_int4<0, ROWS>), dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in,
-                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.H, 2 * F, F, upe);
+            hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D>), grid, dim3(256), 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, d.H, 2 * F, F, upe,
+                               sparse);
         else
-            hipLaunchKernelGGL((k_gemm_int4<1, ROWS>), dim3(d.E * upe), dim3(256), 0, s, (const uint16_t*)in,
-                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, F, d.H, d.H, upe);
+            hipLaunchKernelGGL((k_gemm_int4<1, ROWS, D>), grid, dim3(256), 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, F, d.H, d.H, upe,
+                               sparse);
     };
-    if ((long long)d.T * d.K <= 8ll * d.E) go(std::integral_constant<int, 16>{});
-    else go(std::integral_constant<int, 32>{});
+    using std::integral_constant;
+    if (avg > 8) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+    else if (units <= num_cu) go(integral_constant<int, 16>{}, integral_constant<int, 6>{});
+    else if (units <= 2 * num_cu) go(integral_constant<int, 16>{}, integral_constant<int, 3>{});
+    else go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
     return hipGetLastError();
 }
 

@@ -104,7 +104,7 @@ size_t fp8_mlp_scratch_bytes(long long R, int H, int F);
 // 1 FC2 (bf16 activations -> bf16 expert output); rows without a copy are
 // not written
 hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* in, const void* w, const float* ws,
-                            void* out, hipStream_t s);
+                            void* out, int num_cu, hipStream_t s);
 // layer norm of rows and its backward pass; the gate and its backward pass
 size_t norm_backward_scratch_bytes(int T, int H);
 hipError_t launch_layer_norm(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x, const void* weight,
