@@ -44,16 +44,18 @@ constexpr int kUnitBytes = 4 * kWaveBytes;
 constexpr int kBlock = 2;             // steps that share a transfer of scales: 4 groups of 32 rows
 constexpr int kScaleBytes = 32 * 4 * 4;
 
-// LDS of a kernel for passes of up to `rows` token rows with `depth` steps in
-// the ring: the ring, and two blocks of scales per wavefront (more in a deeper
-// ring: a block is read until depth - 1 steps after the next one's transfer).
-constexpr int scale_blocks(int depth) { return (depth + kBlock - 1) / kBlock + 1; }
-constexpr int lds_bytes(int rows, int depth) {
-    return scale_blocks(depth) * 4 * kScaleBytes + depth * (kUnitBytes + rows * kCols * 2);
+// LDS of a kernel for passes of up to `rows` token rows: for each of its
+// `split` sets of four wavefronts the ring of `depth` steps and the blocks of
+// scales per wavefront that may still be read while the ring's are loaded.
+constexpr int scale_blocks(int depth, int split) { return split > 1 ? depth : (depth + kBlock - 1) / kBlock + 1; }
+constexpr int set_bytes(int rows, int depth, int split) {
+    return scale_blocks(depth, split) * 4 * kScaleBytes + depth * (kUnitBytes + rows * kCols * 2);
 }
+constexpr int lds_bytes(int rows, int depth, int split) { return split * set_bytes(rows, depth, split); }
 // Workgroups per CU that fit its 160 KB.
-constexpr int per_cu(int rows, int depth) { return 160 * 1024 / lds_bytes(rows, depth); }
-static_assert(per_cu(16, 2) == 3 && per_cu(16, 3) == 2 && per_cu(16, 6) == 1 && per_cu(32, 2) == 2, "LDS budget");
+constexpr int per_cu(int rows, int depth, int split) { return 160 * 1024 / lds_bytes(rows, depth, split); }
+static_assert(per_cu(16, 2, 1) == 3 && per_cu(16, 3, 1) == 2 && per_cu(16, 3, 2) == 1 && per_cu(32, 2, 1) == 2,
+              "LDS budget");
 
 // Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
 // (wave-uniform) + voff (per lane) to LDS byte address lds + 16 * lane (4 *
@@ -120,18 +122,23 @@ constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 of -24
 // weight tiles at t0 / t1 (byte 0 of each tile's first row) with scales at ws0
 // and, scale_step bytes further, for the second tile.  On return lane l holds,
 // for token 16 t + 4 * (l / 16) + j of the pass, the sums of the tiles' rows l
-// % 16 in acc[.][t][j].
-template <int ROWS, int D>
+// % 16 in acc[.][t][j] (of the first set; `lds` is the set's own part of the
+// workgroup's `shared`).
+template <int ROWS, int D, int SPLIT>
 __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
-                                                int Kdim, int lane, int wave, unsigned char* lds,
-                                                f32x4 (&acc)[2][(ROWS + 15) / 16]) {
-    constexpr int NTB = (ROWS + 15) / 16, TL = ROWS / 8, SB = scale_blocks(D), kScaleRing = SB * 4 * kScaleBytes;
-    constexpr int kLoads = 4 + TL;         // transfers of a wavefront per step, but for the scales
+                                                int Kdim, int lane, int wave, int set, unsigned char* lds,
+                                                unsigned char* shared, f32x4 (&acc)[2][(ROWS + 15) / 16]) {
+    constexpr int NTB = (ROWS + 15) / 16, TL = ROWS / 8, SB = scale_blocks(D, SPLIT), kScaleRing = SB * 4 * kScaleBytes;
+    // transfers of a wavefront per step (but for the scales where not every step has its own)
+    constexpr int kLoads = 4 + TL + (SPLIT > 1);
     constexpr int kStage = kUnitBytes + ROWS * kCols * 2;
     const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2, groups = Kdim / 128;
     const int steps = (Kdim + kCols - 1) / kCols;
     const bool half_last = Kdim % kCols != 0;   // the last step holds one group only
+    // this set's steps: its i-th is step i * SPLIT + set
+    const int own = (steps - set + SPLIT - 1) / SPLIT, most = (steps + SPLIT - 1) / SPLIT;
+    auto block_slot = [&](int i) { return SPLIT > 1 ? i % SB : i / kBlock % SB; };
 #pragma unroll
     for (int t = 0; t < NTB; ++t) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -159,20 +166,22 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     gchar* bx = uniform_ptr(X + (size_t)row0 * Kdim);
     const uint32_t ring = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
-    auto load_scales = [&](int blk) {
-        const uint32_t at = ring + (uint32_t)(blk % SB * 4 + wave) * kScaleBytes;
+    auto load_scales = [&](int i) {
+        const int blk = (i * SPLIT + set) / kBlock;
+        const uint32_t at = ring + (uint32_t)(block_slot(i) * 4 + wave) * kScaleBytes;
         if (wide) {
             if (lane < 32) to_lds16(bs, scale_off(lane, 4 * blk), at);
         } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                to_lds4(bs, scale_off(16 * i + (lane >> 2), min(4 * blk + (lane & 3), groups - 1)), at + 256 * i);
+            for (int j = 0; j < 2; ++j)
+                to_lds4(bs, scale_off(16 * j + (lane >> 2), min(4 * blk + (lane & 3), groups - 1)), at + 256 * j);
         }
     };
-    auto load = [&](int k) {
-        if (k % kBlock == 0) load_scales(k / kBlock);
+    auto load = [&](int i) {
+        if (SPLIT > 1 || i % kBlock == 0) load_scales(i);
+        const int k = i * SPLIT + set;
         const bool last = k == steps - 1;
-        const uint32_t at = ring + kScaleRing + (uint32_t)(k % D) * kStage;
+        const uint32_t at = ring + kScaleRing + (uint32_t)(i % D) * kStage;
         const uint32_t aw = at + (uint32_t)wave * kWaveBytes;
         const size_t line = (size_t)k * 128;
         const uint32_t wo = last ? woff_last : woff;
@@ -187,10 +196,11 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     };
     const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
     const CodeBits bits;
-    auto group = [&](int k, int slot, int half) {
+    auto group = [&](int i0, int slot, int half) {
         const unsigned char* st = lds + kScaleRing + slot * kStage;
         const unsigned char* sw = st + wave * kWaveBytes;
-        const float* ss = (const float*)(lds + (k / kBlock % SB * 4 + wave) * kScaleBytes) + 2 * (k % kBlock) + half;
+        const float* ss = (const float*)(lds + (block_slot(i0) * 4 + wave) * kScaleBytes) +
+                          2 * ((i0 * SPLIT + set) % kBlock) + half;
         u32x4 b[2][4];
         float sc[2];
 #pragma unroll
@@ -224,44 +234,59 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     wait_vm<0>();      // the counts below are of the transfers alone
     lds_barrier();     // nobody reads the previous pass's ring any more
 #pragma unroll
-    for (int k = 0; k < D - 1; ++k)
-        if (k < steps) load(k);
-    auto arrive = [&](int k) {
-        // Step k has landed; the transfers of up to D - 2 steps after it may be in flight.  They complete in order,
-        // and counting the scales' among the steps' only waits for a little more.
-        const int later = min(D - 2, steps - 1 - k);
-        if (later >= 4) wait_vm<4 * kLoads>();
-        else if (later == 3) wait_vm<3 * kLoads>();
-        else if (later == 2) wait_vm<2 * kLoads>();
-        else if (later == 1) wait_vm<kLoads>();
+    for (int i = 0; i < D - 1; ++i)
+        if (i < own) load(i);
+    auto arrive = [&](int i) {
+        // The set's step i has landed; the transfers of up to D - 2 steps after it may be in flight.  They complete in
+        // order, and counting the scales' among the steps' only waits for a little more.
+        const int later = min(D - 2, own - 1 - i);
+        if (D > 2 && later >= 1) wait_vm<kLoads>();
         else wait_vm<0>();
         lds_barrier();
-        if (k + D - 1 < steps) load(k + D - 1);   // into the slot that step k - 1 was read from
+        if (i + D - 1 < own) load(i + D - 1);   // into the slot that step i - 1 was read from
     };
-    const int whole = steps - (half_last ? 1 : 0);
-    for (int k0 = 0; k0 < whole; k0 += D)
+    static_assert(D <= 3, "arrive() lets one step be in flight");
+    const int common = (steps - (half_last ? 1 : 0)) / SPLIT;   // whole steps that every set has
+    for (int i0 = 0; i0 < common; i0 += D)
 #pragma unroll
-        for (int u = 0; u < D; ++u)   // step k0 + u is in slot u: a constant in every LDS address
-            if (k0 + u < whole) {
-                arrive(k0 + u);
-                group(k0 + u, u, 0);
-                group(k0 + u, u, 1);
+        for (int u = 0; u < D; ++u)   // step i0 + u is in slot u: a constant in every LDS address
+            if (i0 + u < common) {
+                arrive(i0 + u);
+                group(i0 + u, u, 0);
+                group(i0 + u, u, 1);
             }
-    if (half_last) {
-        arrive(whole);
-        group(whole, whole % D, 0);
+    if (common < most) {   // a step that not every set has, or half a step
+        arrive(common);
+        if (common < own) {
+            group(common, common % D, 0);
+            if (!half_last || common * SPLIT + set < steps - 1) group(common, common % D, 1);
+        }
+    }
+    if constexpr (SPLIT > 1) {   // the sets' sums join in the first one
+        static_assert(SPLIT == 2, "one partner");
+        f32x4* part = (f32x4*)shared + (wave * 64 + lane) * 2 * NTB;
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < 2 * NTB; ++j)
+            if (set == 1) part[j] = acc[j / NTB][j % NTB];
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < 2 * NTB; ++j)
+            if (set == 0) acc[j / NTB][j % NTB] += part[j];
     }
 }
 
 // MODE 0: SwiGLU of (gate, up) at feature f0 + l % 16; MODE 1: output rows
 // f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout].
-template <int MODE, int ROWS, int D>
+template <int MODE, int ROWS, int D, int SPLIT>
 __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                           const float* ws0, uint32_t scale_step, uint16_t* __restrict__ Out,
                                           long long row0, int mv, int Kdim, int Nout, int f0, int lane, int wave,
-                                          unsigned char* lds) {
+                                          int set, unsigned char* lds, unsigned char* shared) {
     f32x4 acc[2][(ROWS + 15) / 16];
-    int4_accumulate<ROWS, D>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, lds, acc);
+    int4_accumulate<ROWS, D, SPLIT>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, set, lds, shared,
+                                       acc);
+    if (SPLIT > 1 && set) return;
 #pragma unroll
     for (int t = 0; t < (ROWS + 15) / 16; ++t)
 #pragma unroll
@@ -305,15 +330,16 @@ __device__ __forceinline__ int nth_with_rows(const int32_t* __restrict__ kept, i
 
 // Passes of up to ROWS token rows each: pass blockIdx.y and every gridDim.y-th
 // after it.  `sparse`: blockIdx.x counts the units of the experts that have
-// rows, otherwise of all.  At least per_cu wavefronts per SIMD, two of them to
-// keep matrix results in vector registers.
-template <int MODE, int ROWS, int D>
-__global__ __launch_bounds__(256, per_cu(ROWS, D) > 2 ? per_cu(ROWS, D) : 2) void k_gemm_int4(
+// rows, otherwise of all.
+// SPLIT sets of four wavefronts share a unit's steps.
+template <int MODE, int ROWS, int D, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT, SPLIT * per_cu(ROWS, D, SPLIT)) void k_gemm_int4(
     const uint16_t* __restrict__ X, const uint8_t* __restrict__ W, const float* __restrict__ Ws,
     uint16_t* __restrict__ Out, const int64_t* __restrict__ seg_off, const int32_t* __restrict__ kept, long long R,
     int E, int Kdim, int Wrows, int Nout, int units_per_expert, int sparse) {
-    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS, D)];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS, D, SPLIT)];
+    const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = any_wave & 3, set = any_wave >> 2;
     int e = blockIdx.x / units_per_expert;
     const int unit = blockIdx.x - e * units_per_expert;
     if (sparse) e = nth_with_rows(kept, E, e, lane);
@@ -331,8 +357,8 @@ __global__ __launch_bounds__(256, per_cu(ROWS, D) > 2 ? per_cu(ROWS, D) : 2) voi
         const int mv = min(ROWS, me - m0);
         const long long row0 = seg + m0;
         auto pass = [&](auto n) {
-            int4_pass<MODE, decltype(n)::value, D>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0, lane, wave,
-                                                s_ring);
+            int4_pass<MODE, decltype(n)::value, D, SPLIT>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0,
+                                                          lane, wave, set, s_ring + set * set_bytes(ROWS, D, SPLIT), s_ring);
         };
         if (mv <= 8) pass(std::integral_constant<int, 8>{});
         else if (ROWS == 16 || mv <= 16) pass(std::integral_constant<int, 16>{});
@@ -354,25 +380,30 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     const int experts = sparse ? (int)copies : d.E;
     const long long units = (long long)experts * upe;
     const long long avg = (copies + experts - 1) / experts;   // rows per expert, if they are spread evenly
-    auto go = [&](auto rows, auto depth) {
-        constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value;
+    auto go = [&](auto rows, auto depth, auto split) {
+        constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value, SPLIT = decltype(split)::value;
         // passes of their own workgroups while the units alone leave CUs idle
         const long long fill = (2ll * num_cu + units - 1) / units, passes = (avg + ROWS - 1) / ROWS;
         const dim3 grid((unsigned)units, (unsigned)(fill < passes ? fill : passes));
         if (stage == 0)
-            hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D>), grid, dim3(256), 0, s, (const uint16_t*)in,
+            hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D, SPLIT>), grid, dim3(256 * SPLIT), 0, s, (const uint16_t*)in,
                                (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, d.H, 2 * F, F, upe,
                                sparse);
         else
-            hipLaunchKernelGGL((k_gemm_int4<1, ROWS, D>), grid, dim3(256), 0, s, (const uint16_t*)in,
+            hipLaunchKernelGGL((k_gemm_int4<1, ROWS, D, SPLIT>), grid, dim3(256 * SPLIT), 0, s, (const uint16_t*)in,
                                (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, F, d.H, d.H, upe,
                                sparse);
     };
     using std::integral_constant;
-    if (avg > 8) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-    else if (units <= num_cu) go(integral_constant<int, 16>{}, integral_constant<int, 6>{});
-    else if (units <= 2 * num_cu) go(integral_constant<int, 16>{}, integral_constant<int, 3>{});
-    else go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    integral_constant<int, 1> one;
+    integral_constant<int, 2> two;
+    integral_constant<int, 3> three;
+    integral_constant<int, 16> r16;
+    integral_constant<int, 32> r32;
+    if (avg > 8) go(r32, two, one);
+    else if (units <= num_cu) go(r16, three, two);
+    else if (units <= 2 * num_cu) go(r16, three, one);
+    else go(r16, two, one);
     return hipGetLastError();
 }
 

@@ -102,6 +102,9 @@ CASES = [
     (70, 5, 2, 640, 384, 8, None, 0, 2),            # 70 rows: a second pass
     (200, 4, 2, 512, 256, 1, 33, 0, 0),             # capacity drops copies
     (64, 32, 8, 2048, 1024, 2, None, 30, None),
+    (20, 40, 3, 1024, 1024, 1, None, 5, None),      # many units of few rows
+    (90, 100, 2, 384, 640, 3, None, 0, 7),          # the same with odd groups, and one expert of 90 rows
+    (150, 64, 2, 512, 1024, 1, None, 0, None),
     (5, 4, 2, 256, 128, 1, None, 10, None),         # nothing routed
     (0, 4, 2, 256, 128, 1, None, 0, None),
 ]
