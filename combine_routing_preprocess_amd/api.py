@@ -31,7 +31,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream():
     # the current stream's handle, without building a Stream object (2.9 us of a call that launches in 4)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(cond: bool, msg: str):
@@ -77,9 +77,10 @@ def _check_rows(t, name, shape, dtypes):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_current_device(**tensors):
-    current = torch.cuda.current_device() if torch.cuda.is_initialized() else None     # a CPU tensor's is -1
-    for name, t in tensors.items():
+def _check_current_device(tensors):
+    """``tensors``: (name, tensor or None) pairs."""
+    current = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None     # a CPU tensor's is -1
+    for name, t in tensors:
         if t is not None and t.get_device() != current:
             raise ValueError(f"{name} must live on the current GPU")
 
@@ -115,7 +116,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
     _check_rows(mean, "mean", (T,), _F32)
     _check_rows(rstd, "rstd", (T,), _F32)
-    _check_current_device(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    _check_current_device((("x", x), ("weight", weight), ("bias", bias), ("out", out), ("mean", mean),
+                           ("rstd", rstd)))
     A.check(A.lib().moe_layer_norm(T, H, _ROW_DT[x.dtype], _ROW_DT[out.dtype], wdt, _ptr(x), _ptr(weight), _ptr(bias),
                                    float(eps), _ptr(out), _ptr(mean), _ptr(rstd), _stream()), "moe_layer_norm")
     return out, mean, rstd
@@ -159,8 +161,9 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
             raise ValueError(f"scratch holds fewer than the {need} bytes needed")
     else:
         _need(grad_weight is None and grad_bias is None, "grad_weight and grad_bias need want_params")
-    _check_current_device(grad_y=grad_y, x=x, mean=mean, rstd=rstd, weight=weight, out=out, grad_weight=grad_weight,
-                          grad_bias=grad_bias, scratch=scratch)
+    _check_current_device((("grad_y", grad_y), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight),
+                           ("out", out), ("grad_weight", grad_weight), ("grad_bias", grad_bias),
+                           ("scratch", scratch)))
     nbytes = 0 if scratch is None else scratch.numel() * scratch.element_size()
     A.check(A.lib().moe_layer_norm_backward(T, H, _ROW_DT[x.dtype], _ROW_DT[grad_y.dtype], wdt, _ptr(grad_y), _ptr(x),
                                             _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(out), _ptr(grad_weight),
@@ -250,7 +253,6 @@ class Dispatcher:
         return (self.T, self.E) if self.route_fmt == A.ROUTE_SPARSE_BOOL else (self.T, self.K)
 
     def _check_gate(self, logits, score):
-        self._dev(logits, "logits")
         _check_rows(logits, "logits", (self.T, self.E), _ROW_DT)
         if score not in _SCORE:
             raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
@@ -264,17 +266,17 @@ class Dispatcher:
         steers the choice only; -inf logits switch experts off."""
         self._check_gate(logits, score)
         if bias is not None:
-            self._dev(bias, "bias")
             _check_rows(bias, "bias", (self.E,), _F32)
         shape = self._routing_shape()
-        given = routing is not None or probs is not None
         if routing is None:
             routing = torch.empty(shape, dtype=_ROUTING_OUT[self.route_fmt], device=self.device)
+        else:
+            _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
         if probs is None:
             probs = torch.empty(shape, dtype=torch.float32, device=self.device)
-        if given:
-            self._check_routing(routing, probs, None)
-        _check_current_device(logits=logits)
+        else:
+            _check_rows(probs, "probs", shape, _F32)
+        _check_current_device((("logits", logits), ("bias", bias), ("routing", routing), ("probs", probs)))
         A.check(A.lib().moe_gate(C.byref(self.h), _ptr(logits), _ROW_DT[logits.dtype], _ptr(bias), _SCORE[score],
                                  1 if normalize else 0, float(scale), _ptr(routing), _ptr(probs), _stream()),
                 "moe_gate")
@@ -286,13 +288,14 @@ class Dispatcher:
         """Gradient of the gate's weights (grad_probs, in the routing's shape,
         as combine_backward gives it) to the logits [T,E], in their dtype."""
         self._check_gate(logits, score)
-        self._check_routing(routing, grad_probs, None)
+        shape = self._routing_shape()
+        _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
+        _check_rows(grad_probs, "grad_probs", shape, _F32)
         if out is None:
             out = torch.empty_like(logits)
         else:
-            self._dev(out, "out")
-            _need(out.dtype == logits.dtype and out.shape == logits.shape, "out must be like logits")
-        _check_current_device(logits=logits)
+            _check_rows(out, "out", logits.shape, (logits.dtype,))
+        _check_current_device((("grad_probs", grad_probs), ("logits", logits), ("routing", routing), ("out", out)))
         A.check(A.lib().moe_gate_backward(C.byref(self.h), _ptr(grad_probs), _ptr(logits), _ROW_DT[logits.dtype],
                                           _ptr(routing), _SCORE[score], 1 if normalize else 0, float(scale),
                                           _ptr(out), _stream()), "moe_gate_backward")
@@ -493,7 +496,7 @@ class Dispatcher:
             out = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device(perm=perm)
+            _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_swiglu_mlp(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                                scratch.numel(), _ptr(out), _stream()), "moe_grouped_swiglu_mlp")
@@ -512,7 +515,7 @@ class Dispatcher:
         self._check_perm(perm, perm_scales)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device(perm=perm)
+            _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_swiglu_mlp_noalloc(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales),
                                                        _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(out),
                                                        _stream()), "moe_grouped_swiglu_mlp_noalloc")
@@ -527,7 +530,7 @@ class Dispatcher:
         self._check_perm(perm, perm_scales)
         self._check_scratch(scratch, F, wdtype)
         if wdtype == "int4":
-            _check_current_device(perm=perm)
+            _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_fc1_swiglu(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(scratch), scratch.numel(), _stream()),
                 "moe_grouped_fc1_swiglu")
@@ -548,7 +551,7 @@ class Dispatcher:
         self._check_after_fc1(F, wdtype, scratch)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device(out=out)
+            _check_current_device((("out", out),))
         A.check(A.lib().moe_grouped_fc2(C.byref(self.h), F, _DT[wdtype], _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                         scratch.numel(), _ptr(out), _stream()), "moe_grouped_fc2")
         return out
