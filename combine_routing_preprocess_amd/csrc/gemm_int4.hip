@@ -129,10 +129,14 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
                                                 int Kdim, int lane, int wave, int set, unsigned char* lds,
                                                 unsigned char* shared, f32x4 (&acc)[2][(ROWS + 15) / 16]) {
-    constexpr int NTB = (ROWS + 15) / 16, TL = ROWS / 8, SB = scale_blocks(D, SPLIT), kScaleRing = SB * 4 * kScaleBytes;
-    // transfers of a wavefront per step (but for the scales where not every step has its own)
-    constexpr int kLoads = 4 + TL + (SPLIT > 1);
-    constexpr int kStage = kUnitBytes + ROWS * kCols * 2;
+    // Passes of up to 4 rows keep a copy of them per wavefront (in the room of 16 shared ones), so that no wavefront
+    // waits for another.
+    constexpr bool kOwnRows = ROWS <= 4;
+    constexpr int NTB = (ROWS + 15) / 16, TL = kOwnRows ? 2 : ROWS / 8, SB = scale_blocks(D, SPLIT), kScaleRing = SB * 4 * kScaleBytes;
+    // transfers of a wavefront per step, at least (scales where every step has its own; one of two token rows or more)
+    constexpr int kLoads = 4 + (kOwnRows ? 1 : TL) + (SPLIT > 1);
+    constexpr int kStage = kUnitBytes + (kOwnRows ? 16 : ROWS) * kCols * 2;
+    const int own_rows_at = kOwnRows ? wave * 4 * kCols * 2 : 0;
     const int r16 = lane & 15, c1 = lane >> 4, row_bytes = Kdim / 2, groups = Kdim / 128;
     const int steps = (Kdim + kCols - 1) / kCols;
     const bool half_last = Kdim % kCols != 0;   // the last step holds one group only
@@ -157,7 +161,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     uint32_t xoff[TL], xoff_last[TL];
 #pragma unroll
     for (int j = 0; j < TL; ++j) {
-        const int r = 2 * (wave + 4 * j) + (lane >> 5), p = (lane & 31) ^ (r & 15);
+        const int r = 2 * (kOwnRows ? j : wave + 4 * j) + (lane >> 5), p = (lane & 31) ^ (r & 15);
         const uint32_t at = (uint32_t)min(r, mv - 1) * (uint32_t)Kdim * 2u;
         xoff[j] = at + 16u * (uint32_t)p;
         xoff_last[j] = at + 16u * (uint32_t)(half_last ? p & 15 : p);
@@ -191,8 +195,9 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
         to_lds16_once(b1 + line + 8 * (size_t)row_bytes, wo, aw + 3072);
 #pragma unroll
         for (int j = 0; j < TL; ++j)
-            to_lds16(bx + (size_t)k * (kCols * 2), last ? xoff_last[j] : xoff[j],
-                     at + kUnitBytes + (uint32_t)(wave + 4 * j) * 1024);
+            if (!kOwnRows || j == 0 || mv > 2)
+                to_lds16(bx + (size_t)k * (kCols * 2), last ? xoff_last[j] : xoff[j],
+                         at + kUnitBytes + (uint32_t)(own_rows_at + (kOwnRows ? j : wave + 4 * j) * 1024));
     };
     const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
     const CodeBits bits;
@@ -217,7 +222,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
             f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                a[q] = pair_order(*(const u32x4*)(st + kUnitBytes + r * (kCols * 2) +
+                a[q] = pair_order(*(const u32x4*)(st + kUnitBytes + own_rows_at + r * (kCols * 2) +
                                                   16 * ((16 * half + 4 * c1 + q) ^ (r & 15))));
 #pragma unroll
             for (int q = 0; q < 4; ++q) z = mfma_bf16(a[q], off, z);
@@ -242,7 +247,8 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
         const int later = min(D - 2, own - 1 - i);
         if (D > 2 && later >= 1) wait_vm<kLoads>();
         else wait_vm<0>();
-        lds_barrier();
+        if (kOwnRows) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        else lds_barrier();
         if (i + D - 1 < own) load(i + D - 1);   // into the slot that step i - 1 was read from
     };
     static_assert(D <= 3, "arrive() lets one step be in flight");
@@ -360,7 +366,8 @@ __global__ __launch_bounds__(256 * SPLIT, SPLIT * per_cu(ROWS, D, SPLIT)) void k
             int4_pass<MODE, decltype(n)::value, D, SPLIT>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0,
                                                           lane, wave, set, s_ring + set * set_bytes(ROWS, D, SPLIT), s_ring);
         };
-        if (mv <= 8) pass(std::integral_constant<int, 8>{});
+        if (ROWS == 16 && mv <= 4) pass(std::integral_constant<int, 4>{});
+        else if (ROWS > 16 && mv <= 8) pass(std::integral_constant<int, 8>{});
         else if (ROWS == 16 || mv <= 16) pass(std::integral_constant<int, 16>{});
         else pass(std::integral_constant<int, ROWS>{});
     }
