@@ -247,7 +247,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
                                                               int G, const void* __restrict__ weight, int wdtype,
                                                               XT* __restrict__ gx, float* __restrict__ pw,
                                                               float* __restrict__ pb, long long pstride) {
-    extern __shared__ float s_cols[];   // [2][H], G > 1 only
+    extern __shared__ float s_cols[];   // [groups that hand over][2][columns], G > 1 only
     __shared__ float2 s_part[2][kMaxWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int grp = wave / W, part = wave - grp * W;
@@ -333,27 +333,35 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward(const YT* __restri
         if (row0 + stride < T) step(1);
     }
     if (!pw && !pb) return;
-    if (G > 1) {   // the row groups' columns, one group after the other
-        for (int turn = 0; turn < G; ++turn) {
-            if (grp == turn) {
+    // the row groups' columns join by halves: groups s .. 2s-1 hand theirs to groups 0 .. s-1
+    const int span = W * NC * 512;   // columns that a group holds, those past H among them
+    for (int half = 8; half >= 1; half >>= 1) {
+        if (half >= G) continue;
+        if (half < 8 && 2 * half < G) __syncthreads();   // the step before has been read
+        float4* at = (float4*)(s_cols + (size_t)2 * span * (grp % half)) + (part * 64 + lane) * 2;
+        if (grp >= half && grp < 2 * half && grp < G) {
 #pragma unroll
-                for (int k = 0; k < NC; ++k)
+            for (int k = 0; k < NC; ++k)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < n[k]) {
-                            float* pa = s_cols + col[k] + i;
-                            pa[0] = turn ? pa[0] + aw[k][i] : aw[k][i];
-                            pa[H] = turn ? pa[H] + ab[k][i] : ab[k][i];
-                        }
-            }
-            __syncthreads();
+                for (int i = 0; i < 2; ++i) {
+                    at[k * W * 128 + i] = make_float4(aw[k][4 * i], aw[k][4 * i + 1], aw[k][4 * i + 2], aw[k][4 * i + 3]);
+                    at[span / 4 + k * W * 128 + i] = make_float4(ab[k][4 * i], ab[k][4 * i + 1], ab[k][4 * i + 2],
+                                                                 ab[k][4 * i + 3]);
+                }
         }
-        for (int h = threadIdx.x; h < H; h += blockDim.x) {
-            if (pw) pw[(long long)blockIdx.x * pstride + h] = s_cols[h];
-            if (pb) pb[(long long)blockIdx.x * pstride + h] = s_cols[H + h];
+        __syncthreads();
+        if (grp < half && grp + half < G) {
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 u = at[k * W * 128 + i], v = at[span / 4 + k * W * 128 + i];
+                    aw[k][4 * i] += u.x; aw[k][4 * i + 1] += u.y; aw[k][4 * i + 2] += u.z; aw[k][4 * i + 3] += u.w;
+                    ab[k][4 * i] += v.x; ab[k][4 * i + 1] += v.y; ab[k][4 * i + 2] += v.z; ab[k][4 * i + 3] += v.w;
+                }
         }
-        return;
     }
+    if (grp > 0) return;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
         if (pw) store_chunk<TAIL>(pw + (long long)blockIdx.x * pstride + col[k], n[k], aw[k]);
@@ -421,7 +429,13 @@ void row_shape(int H, int wide, int* NC, int* W) {
 }
 constexpr int kForwardWide = 8, kBackwardWide = kMaxWaves;
 
-int backward_blocks(int T, int G) { return min(kBackwardBlocks, (int)(((long long)T + G - 1) / G)); }
+// Workgroups of the backward pass.  Each writes 2 H partial sums, the traffic of two bf16 rows and more; rows in
+// series cost a workgroup about a microsecond each while the GPU is not full.  So one row per row group up to 64
+// workgroups, two from there on (256 rows of 7168: 11.5 us with two, 13.1 with one, 12.2 with four).
+int backward_blocks(int T, int G) {
+    const long long one = ((long long)T + G - 1) / G, two = (one + 1) / 2;
+    return (int)(one <= 64 ? one : two <= 64 ? 64 : two < kBackwardBlocks ? two : kBackwardBlocks);
+}
 
 // Calls go with the row types, the steps per lane and whether rows end inside
 // a chunk.
@@ -491,7 +505,10 @@ hipError_t launch_layer_norm_backward(int T, int H, int x_dtype, int y_dtype, in
         float* part = (float*)scratch;
         float* pw = nb == 1 ? gw : params ? part : nullptr;
         float* pb = nb == 1 ? gb : params ? part + H : nullptr;
-        const size_t lds = params && G > 1 ? (size_t)2 * H * sizeof(float) : 0;
+        int half = 0;   // groups of the first joining step
+        for (int i = 8; i >= 1 && !half; i >>= 1)
+            if (i < G) half = i;
+        const size_t lds = params ? (size_t)half * 2 * W * NC * 512 * sizeof(float) : 0;
         auto go = [&](auto xt, auto yt, auto nc, auto tail) {
             using XT = decltype(xt);
             using YT = decltype(yt);
