@@ -7,15 +7,27 @@
 // A few rows per expert share each weight, so streaming the codes bounds it:
 // (1/2 + 4/128) bytes per weight from HBM, against a few multiply-adds each.
 //
-//  * Work unit = (expert, 64 features) for FC1, (expert, 128 output rows) for
-//    FC2, one workgroup of four wavefronts per unit; a wavefront owns two
-//    16-row weight tiles (FC1: the gate and up rows of 16 features).  Per step
-//    a unit takes one 128-byte line (256 codes) of every weight row, the
-//    line's scales (four steps' at a time) and the same 256 columns of its token rows, all straight
-//    from memory into an LDS ring (no registers, no write to LDS by the
-//    wavefronts); the weights and scales are the wavefront's own, the tokens
-//    are shared.  A step's data is loaded D - 1 steps ahead, so two workgroups
-//    per CU keep 64 KB in flight; one wait and one barrier per step.
+//  * Work unit = (expert, 16 features per wavefront) for FC1, (expert, 32
+//    output rows per wavefront) for FC2, one workgroup of four or eight
+//    wavefronts per unit; a wavefront owns two 16-row weight tiles (FC1: the
+//    gate and up rows of its features).  Per step a unit takes one 128-byte
+//    line (256 codes) of every weight row, the line's scales (two steps' at a
+//    time) and the same 256 columns of its token rows, all straight from
+//    memory into an LDS ring: no registers, no LDS writes by the wavefronts.
+//    Weights and scales are the wavefront's own, tokens are shared (passes of
+//    up to four rows have a copy per wavefront and no barriers).  Without the
+//    arithmetic the transfers alone run at 6.8 TB/s.
+//  * The loop is balanced between those transfers and some 160 vector and 24
+//    matrix instructions per step and wavefront, so that many steps have to
+//    overlap on a CU: three workgroups of two ring slots each (64 tokens, 256
+//    experts top-8, 7168 x 2048: 876 us, against 914 with two workgroups of
+//    three slots).  Where a CU gets one or two units the ring is deeper, and
+//    two sets of wavefronts take every other step of a lone unit (one token:
+//    43.5 us against 49).
+//  * Rows per pass: 16 while the shape makes up to 8 rows per expert likely,
+//    then 32, and above 32 a unit of eight wavefronts and 64 rows, which
+//    shares the tokens among more weight rows (32 experts of 256 rows, 2048 x
+//    1024: 278 us against 326, 370 TFLOP/s).  More rows take more passes.
 //  * Products on v_mfma_f32_16x16x32_bf16: token rows are the A operand
 //    (16 rows), weight rows the B operand (16 columns), so a lane dequantises
 //    and scales one weight row only.  A lane's 16-byte piece holds 32
@@ -30,7 +42,6 @@
 //  * After a group's MFMAs the fp32 block sum times the lane's scale is added
 //    to the accumulator: scales are never rounded.  Activations between FC1
 //    and FC2 are rounded once to bf16, as on the bf16 path.
-//  * Up to 32 token rows per pass; more rows take more passes.
 #include "device_ops.h"
 
 namespace moe {
@@ -40,21 +51,24 @@ using namespace ops;
 
 constexpr int kCols = 256;            // columns of a step: a 128-byte line of codes, two scale groups
 constexpr int kWaveBytes = 32 * 128;  // codes of a wavefront's step
-constexpr int kUnitBytes = 4 * kWaveBytes;
+constexpr int kWide = 32;             // rows per expert above which a unit has eight wavefronts
 constexpr int kBlock = 2;             // steps that share a transfer of scales: 4 groups of 32 rows
 constexpr int kScaleBytes = 32 * 4 * 4;
 
-// LDS of a kernel for passes of up to `rows` token rows: for each of its
-// `split` sets of four wavefronts the ring of `depth` steps and the blocks of
-// scales per wavefront that may still be read while the ring's are loaded.
+// LDS of a kernel for passes of up to `rows` token rows and units of `waves`
+// wavefronts: for each of the `split` sets that share a unit's columns the
+// ring of `depth` steps and the blocks of scales per wavefront that may still
+// be read while the ring's are loaded.
 constexpr int scale_blocks(int depth, int split) { return split > 1 ? depth : (depth + kBlock - 1) / kBlock + 1; }
-constexpr int set_bytes(int rows, int depth, int split) {
-    return scale_blocks(depth, split) * 4 * kScaleBytes + depth * (kUnitBytes + rows * kCols * 2);
+constexpr int set_bytes(int rows, int depth, int split, int waves) {
+    return scale_blocks(depth, split) * waves * kScaleBytes + depth * (waves * kWaveBytes + rows * kCols * 2);
 }
-constexpr int lds_bytes(int rows, int depth, int split) { return split * set_bytes(rows, depth, split); }
 // Workgroups per CU that fit its 160 KB.
-constexpr int per_cu(int rows, int depth, int split) { return 160 * 1024 / lds_bytes(rows, depth, split); }
-static_assert(per_cu(16, 2, 1) == 3 && per_cu(16, 3, 1) == 2 && per_cu(16, 3, 2) == 1 && per_cu(32, 2, 1) == 2,
+constexpr int per_cu(int rows, int depth, int split, int waves) {
+    return 160 * 1024 / (split * set_bytes(rows, depth, split, waves));
+}
+static_assert(per_cu(16, 2, 1, 4) == 3 && per_cu(16, 3, 1, 4) == 2 && per_cu(16, 3, 2, 4) == 1 &&
+                  per_cu(32, 2, 1, 4) == 2 && per_cu(64, 2, 1, 8) == 1,
               "LDS budget");
 
 // Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
@@ -124,7 +138,7 @@ constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 of -24
 // for token 16 t + 4 * (l / 16) + j of the pass, the sums of the tiles' rows l
 // % 16 in acc[.][t][j] (of the first set; `lds` is the set's own part of the
 // workgroup's `shared`).
-template <int ROWS, int D, int SPLIT>
+template <int ROWS, int D, int SPLIT, int WAVES>
 __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
                                                 int Kdim, int lane, int wave, int set, unsigned char* lds,
@@ -132,7 +146,9 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     // Passes of up to 4 rows keep a copy of them per wavefront (in the room of 16 shared ones), so that no wavefront
     // waits for another.
     constexpr bool kOwnRows = ROWS <= 4;
-    constexpr int NTB = (ROWS + 15) / 16, TL = kOwnRows ? 2 : ROWS / 8, SB = scale_blocks(D, SPLIT), kScaleRing = SB * 4 * kScaleBytes;
+    constexpr int NTB = (ROWS + 15) / 16, TL = kOwnRows ? 2 : ROWS / (2 * WAVES), SB = scale_blocks(D, SPLIT);
+    constexpr int kScaleRing = SB * WAVES * kScaleBytes, kUnitBytes = WAVES * kWaveBytes;
+    static_assert(TL > 0 && (kOwnRows || TL * 2 * WAVES == ROWS), "token transfers");
     // transfers of a wavefront per step, at least (scales where every step has its own; one of two token rows or more)
     constexpr int kLoads = 4 + (kOwnRows ? 1 : TL) + (SPLIT > 1);
     constexpr int kStage = kUnitBytes + (kOwnRows ? 16 : ROWS) * kCols * 2;
@@ -161,7 +177,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     uint32_t xoff[TL], xoff_last[TL];
 #pragma unroll
     for (int j = 0; j < TL; ++j) {
-        const int r = 2 * (kOwnRows ? j : wave + 4 * j) + (lane >> 5), p = (lane & 31) ^ (r & 15);
+        const int r = 2 * (kOwnRows ? j : wave + WAVES * j) + (lane >> 5), p = (lane & 31) ^ (r & 15);
         const uint32_t at = (uint32_t)min(r, mv - 1) * (uint32_t)Kdim * 2u;
         xoff[j] = at + 16u * (uint32_t)p;
         xoff_last[j] = at + 16u * (uint32_t)(half_last ? p & 15 : p);
@@ -172,7 +188,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
     auto load_scales = [&](int i) {
         const int blk = (i * SPLIT + set) / kBlock;
-        const uint32_t at = ring + (uint32_t)(block_slot(i) * 4 + wave) * kScaleBytes;
+        const uint32_t at = ring + (uint32_t)(block_slot(i) * WAVES + wave) * kScaleBytes;
         if (wide) {
             if (lane < 32) to_lds16(bs, scale_off(lane, 4 * blk), at);
         } else {
@@ -197,14 +213,14 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
         for (int j = 0; j < TL; ++j)
             if (!kOwnRows || j == 0 || mv > 2)
                 to_lds16(bx + (size_t)k * (kCols * 2), last ? xoff_last[j] : xoff[j],
-                         at + kUnitBytes + (uint32_t)(own_rows_at + (kOwnRows ? j : wave + 4 * j) * 1024));
+                         at + kUnitBytes + (uint32_t)(own_rows_at + (kOwnRows ? j : wave + WAVES * j) * 1024));
     };
     const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
     const CodeBits bits;
     auto group = [&](int i0, int slot, int half) {
         const unsigned char* st = lds + kScaleRing + slot * kStage;
         const unsigned char* sw = st + wave * kWaveBytes;
-        const float* ss = (const float*)(lds + (block_slot(i0) * 4 + wave) * kScaleBytes) +
+        const float* ss = (const float*)(lds + (block_slot(i0) * WAVES + wave) * kScaleBytes) +
                           2 * ((i0 * SPLIT + set) % kBlock) + half;
         u32x4 b[2][4];
         float sc[2];
@@ -284,15 +300,15 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
 
 // MODE 0: SwiGLU of (gate, up) at feature f0 + l % 16; MODE 1: output rows
 // f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout].
-template <int MODE, int ROWS, int D, int SPLIT>
+template <int MODE, int ROWS, int D, int SPLIT, int WAVES>
 __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                           const float* ws0, uint32_t scale_step, uint16_t* __restrict__ Out,
-                                          long long row0, int mv, int Kdim, int Nout, int f0, int lane, int wave,
-                                          int set, unsigned char* lds, unsigned char* shared) {
+                                          long long row0, int mv, int Kdim, int Nout, int f0, bool mine, int lane,
+                                          int wave, int set, unsigned char* lds, unsigned char* shared) {
     f32x4 acc[2][(ROWS + 15) / 16];
-    int4_accumulate<ROWS, D, SPLIT>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, set, lds, shared,
+    int4_accumulate<ROWS, D, SPLIT, WAVES>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, set, lds, shared,
                                        acc);
-    if (SPLIT > 1 && set) return;
+    if (!mine) return;
 #pragma unroll
     for (int t = 0; t < (ROWS + 15) / 16; ++t)
 #pragma unroll
@@ -337,15 +353,15 @@ __device__ __forceinline__ int nth_with_rows(const int32_t* __restrict__ kept, i
 // Passes of up to ROWS token rows each: pass blockIdx.y and every gridDim.y-th
 // after it.  `sparse`: blockIdx.x counts the units of the experts that have
 // rows, otherwise of all.
-// SPLIT sets of four wavefronts share a unit's steps.
-template <int MODE, int ROWS, int D, int SPLIT>
-__global__ __launch_bounds__(256 * SPLIT, SPLIT * per_cu(ROWS, D, SPLIT)) void k_gemm_int4(
+// SPLIT sets of WAVES wavefronts share a unit's steps.
+template <int MODE, int ROWS, int D, int SPLIT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES * SPLIT, WAVES / 4 * SPLIT * per_cu(ROWS, D, SPLIT, WAVES)) void k_gemm_int4(
     const uint16_t* __restrict__ X, const uint8_t* __restrict__ W, const float* __restrict__ Ws,
     uint16_t* __restrict__ Out, const int64_t* __restrict__ seg_off, const int32_t* __restrict__ kept, long long R,
     int E, int Kdim, int Wrows, int Nout, int units_per_expert, int sparse) {
-    __shared__ __attribute__((aligned(16))) unsigned char s_ring[lds_bytes(ROWS, D, SPLIT)];
+    __shared__ __attribute__((aligned(16))) unsigned char s_ring[SPLIT * set_bytes(ROWS, D, SPLIT, WAVES)];
     const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wave = any_wave & 3, set = any_wave >> 2;
+    const int wave = any_wave % WAVES, set = any_wave / WAVES;
     int e = blockIdx.x / units_per_expert;
     const int unit = blockIdx.x - e * units_per_expert;
     if (sparse) e = nth_with_rows(kept, E, e, lane);
@@ -354,7 +370,11 @@ __global__ __launch_bounds__(256 * SPLIT, SPLIT * per_cu(ROWS, D, SPLIT)) void k
     long long me_l = seg < R ? (long long)kept[e] : 0;
     if (seg + me_l > R) me_l = R - seg;
     const int me = (int)me_l;
-    const int f0 = MODE == 0 ? unit * kFeat + wave * 16 : unit * kFeat2 + wave * 32;
+    // the unit's features (FC1) or output rows (FC2); of a last unit that is not whole, wavefronts past the end repeat
+    // the first half without storing it
+    int f0 = (unit * WAVES + wave) * (MODE == 0 ? 16 : 32);
+    const bool mine = set == 0 && f0 < Nout;
+    if (f0 >= Nout) f0 -= WAVES / 2 * (MODE == 0 ? 16 : 32);
     const size_t r0 = (size_t)e * Wrows + f0, step = MODE == 0 ? Nout : 16;
     const uint8_t *t0 = W + r0 * (Kdim / 2), *t1 = t0 + step * (Kdim / 2);
     const float* ws0 = Ws + r0 * (Kdim / 128);
@@ -363,13 +383,24 @@ __global__ __launch_bounds__(256 * SPLIT, SPLIT * per_cu(ROWS, D, SPLIT)) void k
         const int mv = min(ROWS, me - m0);
         const long long row0 = seg + m0;
         auto pass = [&](auto n) {
-            int4_pass<MODE, decltype(n)::value, D, SPLIT>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout, f0,
-                                                          lane, wave, set, s_ring + set * set_bytes(ROWS, D, SPLIT), s_ring);
+            int4_pass<MODE, decltype(n)::value, D, SPLIT, WAVES>(X, t0, t1, ws0, scale_step, Out, row0, mv, Kdim, Nout,
+                                                                 f0, mine, lane, wave, set,
+                                                                 s_ring + set * set_bytes(ROWS, D, SPLIT, WAVES),
+                                                                 s_ring);
         };
-        if (ROWS == 16 && mv <= 4) pass(std::integral_constant<int, 4>{});
-        else if (ROWS > 16 && mv <= 8) pass(std::integral_constant<int, 8>{});
-        else if (ROWS == 16 || mv <= 16) pass(std::integral_constant<int, 16>{});
-        else pass(std::integral_constant<int, ROWS>{});
+        using std::integral_constant;
+        if constexpr (ROWS == 16) {
+            if (mv <= 4) pass(integral_constant<int, 4>{});
+            else pass(integral_constant<int, 16>{});
+        } else if constexpr (ROWS == 32) {
+            if (mv <= 8) pass(integral_constant<int, 8>{});
+            else if (mv <= 16) pass(integral_constant<int, 16>{});
+            else pass(integral_constant<int, 32>{});
+        } else {
+            if (mv <= 16) pass(integral_constant<int, 16>{});
+            else if (mv <= 32) pass(integral_constant<int, 32>{});
+            else pass(integral_constant<int, 64>{});
+        }
     }
 }
 
@@ -380,37 +411,43 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     const moe_desc& d = h->desc;
     const long long R = d.out_rows, copies = (long long)d.T * d.K;
     if (R == 0 || copies == 0) return hipSuccess;
-    const int upe = stage == 0 ? F / kFeat : d.H / kFeat2;
     // experts that can have rows, and units to run; fewer copies than experts: skip the experts without rows by
     // counting (their empty workgroups would hold the CUs' LDS in turns: one token took 50 us in FC1 with them)
     const bool sparse = copies < d.E;
-    const int experts = sparse ? (int)copies : d.E;
-    const long long units = (long long)experts * upe;
+    const int experts = sparse ? (int)copies : d.E, nout = stage == 0 ? F : d.H, per_wave = stage == 0 ? 16 : 32;
     const long long avg = (copies + experts - 1) / experts;   // rows per expert, if they are spread evenly
-    auto go = [&](auto rows, auto depth, auto split) {
-        constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value, SPLIT = decltype(split)::value;
+    auto upe = [&](int waves) { return (nout + waves * per_wave - 1) / (waves * per_wave); };
+    auto go = [&](auto rows, auto depth, auto split, auto waves) {
+        constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value, SPLIT = decltype(split)::value,
+                      WAVES = decltype(waves)::value;
+        const long long units = (long long)experts * upe(WAVES);
         // passes of their own workgroups while the units alone leave CUs idle
         const long long fill = (2ll * num_cu + units - 1) / units, passes = (avg + ROWS - 1) / ROWS;
-        const dim3 grid((unsigned)units, (unsigned)(fill < passes ? fill : passes));
+        const dim3 grid((unsigned)units, (unsigned)(fill < passes ? fill : passes)), block(64 * WAVES * SPLIT);
         if (stage == 0)
-            hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D, SPLIT>), grid, dim3(256 * SPLIT), 0, s, (const uint16_t*)in,
-                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, d.H, 2 * F, F, upe,
-                               sparse);
+            hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D, SPLIT, WAVES>), grid, block, 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, d.H, 2 * F, F,
+                               upe(WAVES), sparse);
         else
-            hipLaunchKernelGGL((k_gemm_int4<1, ROWS, D, SPLIT>), grid, dim3(256 * SPLIT), 0, s, (const uint16_t*)in,
-                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, F, d.H, d.H, upe,
-                               sparse);
+            hipLaunchKernelGGL((k_gemm_int4<1, ROWS, D, SPLIT, WAVES>), grid, block, 0, s, (const uint16_t*)in,
+                               (const uint8_t*)w, ws, (uint16_t*)out, h->seg_off, h->kept, R, d.E, F, d.H, d.H,
+                               upe(WAVES), sparse);
     };
     using std::integral_constant;
     integral_constant<int, 1> one;
     integral_constant<int, 2> two;
     integral_constant<int, 3> three;
+    integral_constant<int, 4> four;
+    integral_constant<int, 8> eight;
     integral_constant<int, 16> r16;
     integral_constant<int, 32> r32;
-    if (avg > 8) go(r32, two, one);
-    else if (units <= num_cu) go(r16, three, two);
-    else if (units <= 2 * num_cu) go(r16, three, one);
-    else go(r16, two, one);
+    integral_constant<int, 64> r64;
+    const long long units = (long long)experts * upe(4);
+    if (avg > kWide) go(r64, two, one, eight);
+    else if (avg > 8) go(r32, two, one, four);
+    else if (units <= num_cu) go(r16, three, two, four);
+    else if (units <= 2 * num_cu) go(r16, three, one, four);
+    else go(r16, two, one, four);
     return hipGetLastError();
 }
 
