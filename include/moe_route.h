@@ -252,7 +252,9 @@ size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype);
  *          stay bf16 (bf16 payload only), products and scales are fp32, a is
  *          rounded once to bf16 before FC2 as with bf16 weights; requires H,
  *          F multiples of 128.  Rows that hold no kept copy are not written.
- *          Built for decode-sized batches, as fp8.
+ *          A row with an infinity, or with values whose products with 31 (the
+ *          largest code as it is multiplied) leave fp32, gives NaN.  Built for
+ *          decode-sized batches, as fp8.
  *   d_scratch     >= moe_mlp_scratch_bytes bytes
  *   d_expert_out  [R,H] bf16; rows that hold no kept copy are unspecified */
 int moe_grouped_swiglu_mlp(const moe_handle* h, int32_t F, int32_t wdtype, const void* d_perm,

@@ -63,11 +63,6 @@ def _oracle(z, K, bias, score, normalize, scale):
     return idx, w
 
 
-def _dense(routing, probs, d, E, K):
-    """Sparse results as sorted (index, weight) sets for comparison."""
-    return routing.cpu().numpy(), probs.double().cpu().numpy()
-
-
 def _compare(d, fmt, routing, probs, idx, w, E):
     T, K = idx.shape
     r, p = routing.cpu().numpy(), probs.double().cpu().numpy()
@@ -145,6 +140,22 @@ def test_gate_bias_masks_and_nan_keys():
     idx, w = _oracle(z.double().numpy(), 11, bias.double().numpy(), "softmax", False, 1.0)
     _compare(d, "dense_i16", routing, probs, idx, w, 12)
     assert bool((routing[:, 9:] == -1).all())
+
+
+def test_gate_infinite_logits():
+    """+inf is chosen first; the row's softmax weights are NaN, and with a bias
+    the row has no key left.  Other rows are not touched."""
+    z = torch.randn(3, 20, generator=torch.Generator().manual_seed(9))
+    z[1, 7] = float("inf")
+    d = Dispatcher(3, 64, 20, 2, route_fmt="dense_i32", device=DEV)
+    idx, w = _oracle(z[[0, 2]].double().numpy(), 2, None, "softmax", True, 1.0)
+    routing, probs = d.gate(z.to(DEV), normalize=True)
+    assert int(routing[1, 0]) == 7 and bool(torch.isnan(probs[1]).all())
+    _compare(d, "dense_i32", routing[[0, 2]], probs[[0, 2]], idx, w, 20)
+    routing, probs = d.gate(z.to(DEV), score="sigmoid")
+    assert int(routing[1, 0]) == 7 and float(probs[1, 0]) == 1.0
+    routing, probs = d.gate(z.to(DEV), torch.zeros(20, device=DEV))
+    assert routing[1].tolist() == [-1, -1] and probs[1].tolist() == [0.0, 0.0]
 
 
 def test_gate_feeds_preprocess_and_writes_into_given_buffers():

@@ -195,6 +195,55 @@ def test_graph_replay_other_stream_and_shared_experts():
         assert torch.equal(got, Dispatcher(T, H, E, K, route_fmt="dense_i32", device=DEV).layer(x, idx, pr, c1, c2, **kw))
 
 
+def test_two_calls_at_once():
+    """Two dispatchers with their own buffers on two streams at a time give
+    what each gives alone."""
+    T, E, K, H, F = 60, 16, 4, 1024, 512
+    c1, s1 = (t.to(DEV) for t in _weights(E, 2 * F, H, 18))
+    c2, s2 = (t.to(DEV) for t in _weights(E, H, F, 19))
+    streams, runs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for k in range(2):
+        d = Dispatcher(T, H, E, K, route_fmt="dense_i32", device=DEV)
+        x = torch.randn(T, H, generator=torch.Generator().manual_seed(80 + k)).to(BF).to(DEV)
+        idx, z = _route(T, E, K, 81 + k).to(DEV), torch.randn(T, E, generator=torch.Generator().manual_seed(k)).to(DEV)
+        runs.append((d, x, idx, z, d.layer(x, idx, None, c1, c2, w1_scales=s1, w2_scales=s2), d.gate(z), layer_norm(x)))
+    torch.cuda.synchronize()
+    for rep in range(3):
+        got = []
+        for (d, x, idx, z, *_), s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                got.append((d.layer(x, idx, None, c1, c2, w1_scales=s1, w2_scales=s2), d.gate(z), layer_norm(x)))
+        torch.cuda.synchronize()
+        for (y, g, n), (*_, wy, wg, wn) in zip(got, runs):
+            assert torch.equal(y, wy)
+            assert all(torch.equal(p, q) for p, q in zip(g + n, wg + wn))
+
+
+@pytest.mark.parametrize("payload", ["bf16", "fp8"])
+def test_layer_paths_take_norm_and_gate(payload):
+    """layer() with norm, router and gate equals the calls made one by one, on
+    bf16 rows with bf16 weights and on rows quantised on dispatch."""
+    import moe_synth as S
+    T, E, K, H, F = 33, 8, 2, 256, 128
+    g = torch.Generator().manual_seed(61)
+    h, nw, wr = torch.randn(T, H, generator=g).to(BF).to(DEV), torch.ones(H, device=DEV), torch.randn(E, H, generator=g).to(DEV)
+    if payload == "fp8":
+        w1, s1 = (t.to(DEV) for t in S.weights_fp8_blocks(E, 2 * F, H, 62, std=0.05))
+        w2, s2 = (t.to(DEV) for t in S.weights_fp8_blocks(E, H, F, 63, std=0.05))
+    else:
+        w1, w2 = torch.randn(E, 2 * F, H, generator=g).to(BF).to(DEV) * 0.05, torch.randn(E, H, F, generator=g).to(BF).to(DEV) * 0.05
+        s1 = s2 = None
+    d = Dispatcher(T, H, E, K, payload=payload, device=DEV)
+    router = lambda rows: rows.float() @ wr.T
+    got = d.layer(h, None, None, w1, w2, w1_scales=s1, w2_scales=s2, norm=(nw, None, 1e-6), router=router,
+                  gate=dict(normalize=True))
+    x, _, _ = layer_norm(h, nw, None, 1e-6)
+    routing, probs = d.gate(router(x), normalize=True)
+    want = d.layer(x, routing, probs, w1, w2, w1_scales=s1, w2_scales=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool(torch.isfinite(got).all())
+
+
 @pytest.mark.parametrize("fmt,score,normalize,biased", [("dense_i16", "sigmoid", True, True),
                                                         ("sparse_bool", "softmax", False, False)])
 def test_norm_gate_and_int4_layer_together(fmt, score, normalize, biased):
