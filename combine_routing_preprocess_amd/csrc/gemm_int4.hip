@@ -36,7 +36,7 @@
 //  * A code becomes a bf16 by placing its four bits at the top of the
 //    mantissa of 16.0: 16 + c, exact, one shift and one and-or per two codes.
 //    The pairs come out as columns (0,4) (1,5) (2,6) (3,7); the token operand
-//    is permuted the same way.  What is too much, 24 * sum(x) per token and
+//    is permuted the same way (FC1's output is stored so).  What is too much, 24 * sum(x) per token and
 //    group, is an MFMA with a constant -24 operand whose result every tile's
 //    accumulation starts from; it costs no vector instruction.
 //  * After a group's MFMAs the fp32 block sum times the lane's scale is added
@@ -138,7 +138,7 @@ constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 of -24
 // for token 16 t + 4 * (l / 16) + j of the pass, the sums of the tiles' rows l
 // % 16 in acc[.][t][j] (of the first set; `lds` is the set's own part of the
 // workgroup's `shared`).
-template <int ROWS, int D, int SPLIT, int WAVES>
+template <int MODE, int ROWS, int D, int SPLIT, int WAVES>
 __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                                 const float* ws0, uint32_t scale_step, long long row0, int mv,
                                                 int Kdim, int lane, int wave, int set, unsigned char* lds,
@@ -205,10 +205,9 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
         const uint32_t aw = at + (uint32_t)wave * kWaveBytes;
         const size_t line = (size_t)k * 128;
         const uint32_t wo = last ? woff_last : woff;
-        to_lds16_once(b0 + line, wo, aw);
-        to_lds16_once(b0 + line + 8 * (size_t)row_bytes, wo, aw + 1024);
-        to_lds16_once(b1 + line, wo, aw + 2048);
-        to_lds16_once(b1 + line + 8 * (size_t)row_bytes, wo, aw + 3072);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // eight weight rows each
+            to_lds16_once((i < 2 ? b0 : b1) + line + 8 * (i & 1) * (size_t)row_bytes, wo, aw + 1024u * i);
 #pragma unroll
         for (int j = 0; j < TL; ++j)
             if (!kOwnRows || j == 0 || mv > 2)
@@ -217,6 +216,7 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     };
     const u32x4 off = {kMinus24, kMinus24, kMinus24, kMinus24};
     const CodeBits bits;
+    auto tokens = [&](const u32x4& x) { return MODE == 0 ? pair_order(x) : x; };   // FC1 stores its output in pair order
     auto group = [&](int i0, int slot, int half) {
         const unsigned char* st = lds + kScaleRing + slot * kStage;
         const unsigned char* sw = st + wave * kWaveBytes;
@@ -238,8 +238,8 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
             f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                a[q] = pair_order(*(const u32x4*)(st + kUnitBytes + own_rows_at + r * (kCols * 2) +
-                                                  16 * ((16 * half + 4 * c1 + q) ^ (r & 15))));
+                a[q] = tokens(*(const u32x4*)(st + kUnitBytes + own_rows_at + r * (kCols * 2) +
+                                              16 * ((16 * half + 4 * c1 + q) ^ (r & 15))));
 #pragma unroll
             for (int q = 0; q < 4; ++q) z = mfma_bf16(a[q], off, z);
 #pragma unroll
@@ -299,14 +299,15 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
 }
 
 // MODE 0: SwiGLU of (gate, up) at feature f0 + l % 16; MODE 1: output rows
-// f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout].
+// f0 + l % 16 and f0 + 16 + l % 16.  Both stored as bf16 [R, Nout], the
+// activations of MODE 0 with each 8 features in pair order, as FC2 reads them.
 template <int MODE, int ROWS, int D, int SPLIT, int WAVES>
 __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const uint8_t* t0, const uint8_t* t1,
                                           const float* ws0, uint32_t scale_step, uint16_t* __restrict__ Out,
                                           long long row0, int mv, int Kdim, int Nout, int f0, bool mine, int lane,
                                           int wave, int set, unsigned char* lds, unsigned char* shared) {
     f32x4 acc[2][(ROWS + 15) / 16];
-    int4_accumulate<ROWS, D, SPLIT, WAVES>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, set, lds, shared,
+    int4_accumulate<MODE, ROWS, D, SPLIT, WAVES>(X, t0, t1, ws0, scale_step, row0, mv, Kdim, lane, wave, set, lds, shared,
                                        acc);
     if (!mine) return;
 #pragma unroll
@@ -315,7 +316,8 @@ __device__ __forceinline__ void int4_pass(const uint16_t* __restrict__ X, const 
         for (int j = 0; j < 4; ++j) {
             const int tok = 16 * t + 4 * (lane >> 4) + j;
             if (tok >= mv) continue;
-            uint16_t* o = Out + (size_t)(row0 + tok) * Nout + f0 + (lane & 15);
+            const int at = MODE == 0 ? (lane & 8) | ((lane & 3) << 1) | ((lane >> 2) & 1) : lane & 15;
+            uint16_t* o = Out + (size_t)(row0 + tok) * Nout + f0 + at;
             if (MODE == 0) {
                 o[0] = (uint16_t)f32_to_bf16(swiglu(acc[0][t][j], acc[1][t][j]));
             } else {

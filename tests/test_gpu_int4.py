@@ -155,7 +155,10 @@ def test_every_code_and_column_lands_in_its_place():
     scratch = d.alloc_mlp_scratch(F, "int4")
     d.fc1(perm, c1, scratch, w1_scales=s1)
     torch.cuda.synchronize()
-    a = scratch[:T * F * 2].view(BF).view(T, F).double().cpu()
+    # the scratch keeps each 8 features in the order 0 4 1 5 2 6 3 7
+    order = torch.arange(F).view(-1, 8)[:, [0, 4, 1, 5, 2, 6, 3, 7]].flatten()
+    a = torch.empty(T, F, dtype=torch.float64)
+    a[:, order] = scratch[:T * F * 2].view(BF).view(T, F).double().cpu()
     rows = d.row_id.cpu()[:, 0].long()
     deq = _deq(*w1)
     for t in range(T):
