@@ -357,14 +357,14 @@ __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__
             sum = wave_sum_dpp(p);
         }
     }
-    const double inv = 1.0 / sum;
-    p = on ? p * inv : 0.0;
+    // a quotient and not a product with 1 / sum: a share that is all of the sum is exactly 1, its gradient exactly 0
+    p = on ? p / sum : 0.0;
     double dot = 0.0;
     if (!sigmoid || normalize) dot = wave_sum_dpp(g * p);
     const double v = on ? p * rest * (whole ? g : g - dot) * (double)scale : 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        o[i] = whole && l[i] != -INFINITY ? -dot * (exp_neg((double)l[i] - m) * inv) * (double)scale : 0.0;
+        o[i] = whole && l[i] != -INFINITY ? -dot * (exp_neg((double)l[i] - m) / sum) * (double)scale : 0.0;
     // the slots' gradients to their experts, one after the other (a repeated expert adds)
     for (int j = 0; j < K; ++j) {
         const int ej = (int)readlane((uint32_t)e, j);
@@ -470,11 +470,10 @@ __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restr
             sum = wave_sum_dpp(part);
         }
     }
-    const double inv = 1.0 / sum;
     double dot = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = p[i] != 0.0 ? p[i] * inv : 0.0;
+        p[i] = p[i] != 0.0 ? p[i] / sum : 0.0;   // exactly 1 where it is all of the sum
         dot += g[i] * p[i];
     }
     dot = !sigmoid || normalize ? wave_sum_dpp(dot) : 0.0;

@@ -243,6 +243,20 @@ def test_gate_backward(T, E, K, fmt, score, normalize, dtype):
     assert np.all(err <= tol), (err - tol).max()
 
 
+@pytest.mark.parametrize("fmt,E", [("dense_i16", 135), ("sparse_bool", 135), ("dense_i32", 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_backward_of_a_single_normalised_weight_is_zero(fmt, E, score):
+    """One chosen expert has the whole share whatever its logit: its gradient
+    is zero, not a rounding of it."""
+    T = 539
+    z = _logits(T, E, F32, 17).to(DEV)
+    d = Dispatcher(T, 64, E, 1, route_fmt=fmt, device=DEV)
+    routing, probs = d.gate(z, score=score, normalize=True)
+    assert bool(((probs == 1.0) | (probs == 0.0)).all())
+    gp = torch.randn(probs.shape, generator=torch.Generator().manual_seed(18)).to(DEV)
+    assert bool((d.gate_backward(gp, z, routing, score=score, normalize=True) == 0).all())
+
+
 @pytest.mark.parametrize("score,normalize", [("softmax", False), ("softmax", True), ("sigmoid", True),
                                              ("sigmoid", False)])
 def test_gate_backward_agrees_with_differences(score, normalize):
