@@ -181,6 +181,7 @@ class Dispatcher:
         L = A.lib()
         self.device = torch.device(device if device is not None else "cuda")
         self._cuda = self.device.type == "cuda"
+        self._scratch_need = {}
         self.desc = make_desc(T, H, E, K, route_fmt, payload, pad_multiple, capacity, out_rows)
         ws_bytes = int(L.moe_workspace_bytes(C.byref(self.desc)))
         if ws_bytes == 0:
@@ -228,7 +229,7 @@ class Dispatcher:
     # ---- checks ------------------------------------------------------------------
     def _dev(self, t: torch.Tensor, name: str):
         index = t.get_device()               # -1 on the CPU
-        if not (self._cuda and index >= 0 and (index == self.device.index or index == torch.cuda.current_device())
+        if not (self._cuda and index >= 0 and (index == self.device.index or index == torch._C._cuda_getDevice())
                 or t.device == self.device):
             raise ValueError(f"{name} must live on {self.device}")
         if not t.is_contiguous():
@@ -400,7 +401,7 @@ class Dispatcher:
             _need(perm_scales.dtype == torch.float32 and tuple(perm_scales.shape) == (self.R, self.H // 128),
                   "perm_scales must be float32 [R, H/128]")
         else:
-            _need(perm.dtype == torch.bfloat16 and tuple(perm.shape) == (self.R, self.H), "perm must be bf16 [R,H]")
+            _need(perm.dtype == torch.bfloat16 and perm.shape == (self.R, self.H), "perm must be bf16 [R,H]")
             _need(perm_scales is None, "bf16 permuted rows take no scales")
 
     def _check_w1(self, w1: torch.Tensor, w1_scales: Optional[torch.Tensor]):
@@ -409,10 +410,11 @@ class Dispatcher:
         [E, 2F, H/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w1, "w1")
         if self._is_int4(w1, w1_scales):
-            if not (w1.shape[0] == self.E and 2 * w1.shape[2] == self.H and w1.shape[1] % 2 == 0 and w1.shape[1] > 0):
+            experts, rows, packed = w1.shape
+            if not (experts == self.E and 2 * packed == self.H and rows % 2 == 0 and rows > 0):
                 raise ValueError(f"4-bit w1 must be [E, 2F, H/2] = [{self.E}, 2F, {self.H // 2}], "
                                  f"got {tuple(w1.shape)}")
-            return int(w1.shape[1]) // 2, self._check_int4(w1, w1_scales, "w1")
+            return rows // 2, self._check_int4(rows, 2 * packed, w1_scales, "w1")
         _need(w1.dim() == 3 and w1.shape[0] == self.E and w1.shape[2] == self.H and w1.shape[1] % 2 == 0
               and w1.shape[1] > 0, f"w1 must be [E, 2F, H] = [{self.E}, 2F, {self.H}], got {tuple(w1.shape)}")
         F = int(w1.shape[1]) // 2
@@ -424,9 +426,10 @@ class Dispatcher:
         [E, H, F/128] float32 scales) on this device; returns (F, wdtype)."""
         self._dev(w2, "w2")
         if self._is_int4(w2, w2_scales):
-            if not (w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0):
+            experts, rows, packed = w2.shape
+            if not (experts == self.E and rows == self.H and packed > 0):
                 raise ValueError(f"4-bit w2 must be [E, H, F/2] = [{self.E}, {self.H}, F/2], got {tuple(w2.shape)}")
-            return 2 * int(w2.shape[2]), self._check_int4(w2, w2_scales, "w2")
+            return 2 * packed, self._check_int4(rows, 2 * packed, w2_scales, "w2")
         _need(w2.dim() == 3 and w2.shape[0] == self.E and w2.shape[1] == self.H and w2.shape[2] > 0,
               f"w2 must be [E, H, F] = [{self.E}, {self.H}, F], got {tuple(w2.shape)}")
         F = int(w2.shape[2])
@@ -439,11 +442,10 @@ class Dispatcher:
         return (w.dtype == torch.uint8 and w.dim() == 3 and scales is not None and scales.dim() == 3
                 and scales.shape[1] == w.shape[1])
 
-    def _check_int4(self, w, scales, name) -> str:
-        cols = 2 * int(w.shape[2])
-        if self.H % 128 or w.shape[1] % 128 or cols % 128:
+    def _check_int4(self, rows, cols, scales, name) -> str:
+        if self.H % 128 or rows % 128 or cols % 128:
             raise ValueError(f"4-bit {name} needs dimensions that are multiples of 128")
-        shape = (self.E, int(w.shape[1]), cols // 128)
+        shape = (self.E, rows, cols // 128)
         self._dev(scales, name + "_scales")
         if scales.dtype != torch.float32 or scales.shape != shape:
             raise ValueError(f"{name}_scales must be float32 {shape}, got {scales.dtype} {tuple(scales.shape)}")
@@ -464,7 +466,9 @@ class Dispatcher:
 
     def _check_scratch(self, scratch: torch.Tensor, F: int, wdtype: str):
         self._dev(scratch, "scratch")
-        need = self.mlp_scratch_bytes(F, wdtype)
+        need = self._scratch_need.get((F, wdtype))      # a function of the fixed shape alone
+        if need is None:
+            need = self._scratch_need[F, wdtype] = self.mlp_scratch_bytes(F, wdtype)
         if need <= 0:
             raise ValueError(f"invalid FFN width {F} for {wdtype} weights")
         if scratch.numel() * scratch.element_size() < need:
@@ -483,8 +487,8 @@ class Dispatcher:
         (bf16, or e4m3 codes with 128x128 block scales, or packed 4-bit codes
         w1 [E,2F,H/2], w2 [E,H,F/2] with scales [E,2F,H/128], [E,H,F/128]: see
         _check_w1).  With 4-bit weights, rows of ``out`` that hold no kept copy
-        are left as they were.  With a handle of fp8 payload, perm is e4m3 codes quantised on dispatch plus perm_scales
-        (fp8 weights only)."""
+        are left as they were.  With a handle of fp8 payload, perm is e4m3
+        codes quantised on dispatch plus perm_scales (fp8 weights only)."""
         F, wdtype = self._check_w1(w1, w1_scales)
         F2, wdtype2 = self._check_w2(w2, w2_scales)
         _need(F2 == F and wdtype2 == wdtype, "w1 and w2 must share the FFN width and dtype")
@@ -499,7 +503,8 @@ class Dispatcher:
             _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_swiglu_mlp(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(scratch),
-                                               scratch.numel(), _ptr(out), _stream()), "moe_grouped_swiglu_mlp")
+                                               scratch.numel() * scratch.element_size(), _ptr(out), _stream()),
+                "moe_grouped_swiglu_mlp")
         return out
 
     def grouped_mlp_noalloc(self, perm: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, *,
