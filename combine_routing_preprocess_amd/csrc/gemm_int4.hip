@@ -25,23 +25,10 @@
 //    two sets of wavefronts take every other step of a lone unit (one token:
 //    43.5 us against 49).
 //  * Rows per pass: 16 while the shape makes up to 8 rows per expert likely,
-//    then 32, and above 32 a unit of eight wavefronts and 64 rows, which
-//    shares the tokens among more weight rows (32 experts of 256 rows, 2048 x
-//    1024: 278 us against 326, 370 TFLOP/s).  More rows take more passes.
-//  * Products on v_mfma_f32_16x16x32_bf16: token rows are the A operand
-//    (16 rows), weight rows the B operand (16 columns), so a lane dequantises
-//    and scales one weight row only.  A lane's 16-byte piece holds 32
-//    consecutive codes of its row; MFMA q of a 128-column group takes the 8
-//    codes of the piece's word q, and the token operand the same 8 columns.
-//  * A code becomes a bf16 by placing its four bits at the top of the
-//    mantissa of 16.0: 16 + c, exact, one shift and one and-or per two codes.
-//    The pairs come out as columns (0,4) (1,5) (2,6) (3,7); the token operand
-//    is permuted the same way (FC1's output is stored so).  What is too much, 24 * sum(x) per token and
-//    group, is an MFMA with a constant -24 operand whose result every tile's
-//    accumulation starts from; it costs no vector instruction.
-//  * After a group's MFMAs the fp32 block sum times the lane's scale is added
-//    to the accumulator: scales are never rounded.  Activations between FC1
-//    and FC2 are rounded once to bf16, as on the bf16 path.
+//    32 or, in units of eight wavefronts that share the tokens among more
+//    weight rows, 64 above that (32 experts of 256 rows, 2048 x 1024: 278 us
+//    with 64 against 326 with 32, 370 TFLOP/s), as far as the CUs all get a
+//    workgroup.  More rows take more passes.
 #include "device_ops.h"
 
 namespace moe {
@@ -51,7 +38,7 @@ using namespace ops;
 
 constexpr int kCols = 256;            // columns of a step: a 128-byte line of codes, two scale groups
 constexpr int kWaveBytes = 32 * 128;  // codes of a wavefront's step
-constexpr int kWide = 32;             // rows per expert above which a unit has eight wavefronts
+constexpr int kWide = 32;             // rows per expert above which a unit may have eight wavefronts
 constexpr int kBlock = 2;             // steps that share a transfer of scales: 4 groups of 32 rows
 constexpr int kScaleBytes = 32 * 4 * 4;
 
@@ -423,8 +410,9 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
         constexpr int ROWS = decltype(rows)::value, D = decltype(depth)::value, SPLIT = decltype(split)::value,
                       WAVES = decltype(waves)::value;
         const long long units = (long long)experts * upe(WAVES);
-        // passes of their own workgroups while the units alone leave CUs idle
-        const long long fill = (2ll * num_cu + units - 1) / units, passes = (avg + ROWS - 1) / ROWS;
+        // passes of their own workgroups while the units alone leave room on the CUs
+        const long long room = (long long)per_cu(ROWS, D, SPLIT, WAVES) * num_cu;
+        const long long fill = (room + units - 1) / units, passes = (avg + ROWS - 1) / ROWS;
         const dim3 grid((unsigned)units, (unsigned)(fill < passes ? fill : passes)), block(64 * WAVES * SPLIT);
         if (stage == 0)
             hipLaunchKernelGGL((k_gemm_int4<0, ROWS, D, SPLIT, WAVES>), grid, block, 0, s, (const uint16_t*)in,
@@ -444,11 +432,16 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     integral_constant<int, 16> r16;
     integral_constant<int, 32> r32;
     integral_constant<int, 64> r64;
-    const long long units = (long long)experts * upe(4);
-    if (avg > kWide) go(r64, two, one, eight);
-    else if (avg > 8) go(r32, two, one, four);
-    else if (units <= num_cu) go(r16, three, two, four);
-    else if (units <= 2 * num_cu) go(r16, three, one, four);
+    // The largest pass that still gives nearly every CU a workgroup: rows that share a dequantised weight against
+    // CUs at work.  500 tokens, 24 experts of 1152 x 640 (240 units of 64 rows): 38.0 us with 64, 42.1 with 32; 100
+    // tokens, 16 experts of 3584 x 512 (64 units of 64 rows, 256 of 32): 61.9 and 39.1, with 16 rows 44.1; 128 tokens,
+    // 4 experts of 512 x 256 (16, 64 and 128 units): 19.4, 10.8 and 8.8.
+    auto workgroups = [&](int rows, int waves) { return (long long)experts * upe(waves) * ((avg + rows - 1) / rows); };
+    const long long most = workgroups(16, 4);
+    if (avg > kWide && 8 * workgroups(64, 8) >= 7ll * num_cu) go(r64, two, one, eight);
+    else if (avg > 8 && workgroups(32, 4) >= num_cu) go(r32, two, one, four);
+    else if (most <= num_cu) go(r16, three, two, four);
+    else if (most <= 2 * num_cu) go(r16, three, one, four);
     else go(r16, two, one, four);
     return hipGetLastError();
 }

@@ -105,8 +105,10 @@ CASES = [
     (20, 40, 3, 1024, 1024, 1, None, 5, None),      # many units of few rows
     (90, 100, 2, 384, 640, 3, None, 0, 7),          # the same with odd groups, and one expert of 90 rows
     (150, 64, 2, 512, 1024, 1, None, 0, None),
-    (300, 4, 2, 384, 256, 4, None, 7, None),        # 64-row passes; a last unit of FC2 that is half empty
+    (300, 4, 2, 384, 256, 4, None, 7, None),        # many rows of few experts: small passes on many CUs
     (260, 3, 2, 1152, 384, 1, None, 0, 1),          # the same with odd groups and unequal experts
+    (80, 32, 8, 1152, 640, 1, None, 40, 2),         # passes of 32 rows, one expert of three
+    (170, 32, 8, 2176, 1152, 2, None, 0, 3),        # passes of 64 rows; FC2's last unit is half empty
     (5, 4, 2, 256, 128, 1, None, 10, None),         # nothing routed
     (0, 4, 2, 256, 128, 1, None, 0, None),
 ]
