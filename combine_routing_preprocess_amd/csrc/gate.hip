@@ -25,8 +25,11 @@
 //    are looked at only where several do.  The winner is scalar, so lane j
 //    keeps slot j's expert and logit without any exchange.
 //  * exp and the reciprocal below are for arguments that occur here (x <= 0
-//    and 1 <= d <= 2) and take 18 and 6 instructions instead of the library's
-//    general forms.
+//    and 1 <= d <= 2) and take some 20 and 6 instructions instead of the
+//    library's general forms.
+//  * Measured on MI355X, 256 experts top-8 with bias: 8192 tokens in 11.1 us
+//    (the logits alone would take 1.7 us; with shuffles through LDS and the
+//    library's exp 26 us), 16 tokens in 4.8 us; gradient of 8192 tokens 8.9 us.
 #include "wave_ops.h"
 
 namespace moe {

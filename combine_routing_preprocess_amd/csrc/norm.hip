@@ -10,8 +10,13 @@
 // backward reads x and gy and writes gx once.  A row is held in registers by W
 // wavefronts, 8 elements (one chunk) per lane and step, at most NC steps; G
 // rows share a workgroup when they are short.  Workgroups walk the rows with a
-// stride, so weight and bias are loaded once per workgroup, and the next row's
-// loads are issued before the current row's reductions.
+// stride, so weight and bias are loaded once per workgroup, and the loads of
+// the next two rows are in flight during the current row's reductions.
+// Measured on MI355X, 8192 x 7168 bf16: forward 45.7 us (5.1 TB/s), backward
+// 72 us and the sum of its parameter gradients 5 us (together 4.7 TB/s), where
+// a 1 GiB device copy runs at 5.08 TB/s.  The forward takes 2 chunks per lane
+// (7 wavefronts per row; 14 of one chunk: 61 us), the backward one, for the
+// column sums that each lane keeps (two chunks spill: 126 us).
 //
 // Statistics are fp32 and need one barrier per row.  Each wavefront takes the
 // mean m of its own part, then the sum e and the square sum q of what is left,
