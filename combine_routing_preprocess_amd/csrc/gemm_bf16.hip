@@ -101,11 +101,13 @@ __device__ __forceinline__ gchar* uniform_ptr(const char* p) {
 // address = sbase (wave-uniform) + voff (per lane), lane l's 16 bytes land at
 // LDS byte address lds + 16*l.  Inline asm, so the compiler does not treat
 // later LDS reads as dependent on it; completion is awaited explicitly.  m0
-// is written only by these asm statements in this translation unit.
+// is written only by these asm statements in this translation unit; a load to
+// LDS needs one wait state after that (s_nop 0), which the compiler does not
+// add to inline asm.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(gchar* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -548,11 +550,13 @@ static_assert(2 * X_CH == 2 * X_SLOT && NWSET * W_CH == 2 * W_SLOT, "128-row rin
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16v(const void* gptr, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(gptr), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(gptr), "s"(lds)
+                 : "memory", "m0");
 }
 // The same with the non-temporal cache policy, for data read once (weights).
 __device__ __forceinline__ void dma16v_nt(const void* gptr, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(gptr), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(gptr), "s"(lds)
+                 : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

@@ -61,7 +61,9 @@ static_assert(per_cu(16, 2, 1, 4) == 3 && per_cu(16, 3, 1, 4) == 2 && per_cu(16,
 // Memory -> LDS transfers of 16 or 4 bytes per lane: from sbase
 // (wave-uniform) + voff (per lane) to LDS byte address lds + 16 * lane (4 *
 // lane).  Inline asm, so that the compiler does not wait for them before other
-// LDS reads; their completion is awaited explicitly.  m0 is written only here.
+// LDS reads; their completion is awaited explicitly.  m0 is written only here;
+// a load to LDS needs one wait state after that (s_nop 0), which the compiler
+// does not add to inline asm.
 typedef const char __attribute__((address_space(1))) gchar;
 __device__ __forceinline__ gchar* uniform_ptr(const void* p) {
     const uint64_t v = (uint64_t)(uintptr_t)p;
@@ -72,15 +74,15 @@ __device__ __forceinline__ gchar* uniform_ptr(const void* p) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds16(gchar* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds16_once(gchar* sbase, uint32_t voff, uint32_t lds) {   // data read once
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "s"(lds)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds4(gchar* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
