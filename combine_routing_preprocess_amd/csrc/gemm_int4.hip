@@ -161,9 +161,10 @@ __device__ __forceinline__ void int4_accumulate(const uint16_t* __restrict__ X, 
     // it is), so no second set of offsets is kept: 500 tokens, 24 experts of 1152 x 640 take 23.1 + 13.9 us
     // against 23.6 + 14.5 with such a set, and fewer registers spill.
     const uint32_t wback = half_last ? 16u * (uint32_t)(wpiece & 4) : 0u, xback = half_last ? 16u * (lane & 16) : 0u;
-    // Scales of a block lie as [32 rows][4 groups].  Rows of whole 16-byte pieces take one transfer (row lane of
-    // the lower 32 lanes), others two (row 16 i + lane / 4, one group); groups past the row's end repeat its last.
-    const bool wide = groups % 4 == 0;
+    // Scales of a block lie as [32 rows][4 groups].  Rows of whole 16-byte pieces on a base at a multiple of 16 take
+    // one transfer (row lane of the lower 32 lanes), others, for which 4-byte alignment is enough, two (row 16 i +
+    // lane / 4, one group); groups past the row's end repeat its last.
+    const bool wide = groups % 4 == 0 && ((uintptr_t)ws0 & 15) == 0;
     auto scale_off = [&](int row, int g) {
         return (uint32_t)(((row & 15) * groups + g) * 4) + (row & 16 ? scale_step : 0u);
     };

@@ -1,0 +1,42 @@
+"""4-bit expert weights: placements of the scales, live counts, experts that are
+mostly empty, empty batches.  Oracle and tolerances are those of
+test_gpu_int4; calls that differ in placement alone have to agree bit for
+bit."""
+import pytest
+import torch
+
+from combine_routing_preprocess_amd import Dispatcher
+from gpu_util import DEV, log
+from test_gpu_int4 import BF, _check, _route, _weights
+
+pytestmark = pytest.mark.gpu
+
+
+def _shifted(t, floats):
+    """The same values at `floats` floats behind a 256-byte boundary."""
+    room = torch.empty(t.numel() + 64, dtype=t.dtype, device=DEV)
+    assert room.data_ptr() % 256 == 0
+    at = room[floats:floats + t.numel()].view(t.shape)
+    at.copy_(t)
+    return at
+
+
+@pytest.mark.parametrize("floats", [1, 2, 3])
+@pytest.mark.parametrize("T,E,K,H,F", [(2, 16, 4, 1024, 512),        # two sets of wavefronts
+                                       (40, 40, 3, 512, 1024),       # many units of few rows
+                                       (170, 32, 8, 2048, 1024)])    # wide passes
+def test_scales_off_a_16_byte_line(T, E, K, H, F, floats):
+    log("int4 scales shifted", T, E, K, H, F, floats)
+    d = Dispatcher(T, H, E, K, route_fmt="dense_i32", device=DEV)
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).to(BF)
+    perm, *_ = d.dispatch(x.to(DEV), _route(T, E, K, 1).to(DEV))
+    w = _weights(E, 2 * F, H, 2) + _weights(E, H, F, 3)
+    c1, s1, c2, s2 = (t.to(DEV) for t in w)
+    out = torch.full((d.R, H), 7.0, dtype=BF, device=DEV)
+    d.grouped_mlp(perm, c1, c2, w1_scales=_shifted(s1, floats), w2_scales=_shifted(s2, floats), out=out)
+    torch.cuda.synchronize()
+    _check(d, perm, w, out, 7.0)
+    same = torch.full((d.R, H), 7.0, dtype=BF, device=DEV)
+    d.grouped_mlp(perm, c1, c2, w1_scales=s1, w2_scales=s2, out=same)
+    torch.cuda.synchronize()
+    assert torch.equal(same, out)
