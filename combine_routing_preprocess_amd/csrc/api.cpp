@@ -242,13 +242,12 @@ int moe_dispatch(moe_handle* h, const void* d_routing, const float* d_probs, con
 size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype) {
     if (!h || F <= 0) return 0;
     const size_t R = (size_t)h->desc.out_rows;
-    if (wdtype == MOE_BF16) return up(R * (size_t)F * 2, kAlign);
-    if (wdtype == MOE_INT4_G128) return F % 128 || h->desc.H % 128 ? 0 : up(R * (size_t)F * 2, kAlign);
-    if (wdtype == MOE_FP8E4M3_B128) {
-        if (F % 128 || h->desc.H % 128) return 0;
-        return up(fp8_mlp_scratch_bytes((long long)R, h->desc.H, F), kAlign);
-    }
-    return 0;
+    if (wdtype != MOE_BF16 && (F % 128 || h->desc.H % 128)) return 0;
+    size_t n;
+    if (wdtype == MOE_BF16 || wdtype == MOE_INT4_G128) n = R * (size_t)F * 2;
+    else if (wdtype == MOE_FP8E4M3_B128) n = fp8_mlp_scratch_bytes((long long)R, h->desc.H, F);
+    else return 0;
+    return n ? up(n, kAlign) : kAlign;   // 0 is for invalid shapes; no rows is a valid one
 }
 
 namespace {
@@ -284,6 +283,7 @@ int check_mlp(const moe_handle* h, int32_t F, int32_t wdtype, const void* w, con
     if (!scratch) return MOE_EINVAL;
     if (!al16(scratch)) return MOE_EALIGN;
     if (scratch_bytes < moe_mlp_scratch_bytes(h, F, wdtype)) return MOE_ENOSPC;
+    if (h->desc.out_rows == 0) return MOE_OK;   // nothing will be launched
     *ncu = num_cu();
     return *ncu > 0 ? MOE_OK : MOE_EHIP;
 }
@@ -292,8 +292,9 @@ int check_mlp(const moe_handle* h, int32_t F, int32_t wdtype, const void* w, con
 int check_perm(const moe_handle* h, const void* d_perm, const float* d_perm_scales) {
     // fp8 permuted rows (quantised on dispatch) carry their scales; bf16 rows none
     const bool fp8_rows = h->desc.payload == MOE_FP8E4M3_B128;
-    if (fp8_rows != (d_perm_scales != nullptr)) return fp8_rows ? MOE_EINVAL : MOE_EDTYPE;
-    if (!d_perm) return MOE_EINVAL;
+    if (!fp8_rows && d_perm_scales) return MOE_EDTYPE;
+    // an empty array may have no address
+    if (h->desc.out_rows > 0 && (!d_perm || (fp8_rows && !d_perm_scales))) return MOE_EINVAL;
     if (!al16(d_perm) || (d_perm_scales && !al4(d_perm_scales))) return MOE_EALIGN;
     return MOE_OK;
 }
@@ -313,7 +314,7 @@ int check_mlp_host(const moe_handle* h, int32_t F, int32_t wdtype, const void* d
     if (rc) return rc;
     rc = check_perm(h, d_perm, d_perm_scales);
     if (rc) return rc;
-    if (!d_expert_out) return MOE_EINVAL;
+    if (h->desc.out_rows > 0 && !d_expert_out) return MOE_EINVAL;
     return al16(d_expert_out) ? MOE_OK : MOE_EALIGN;
 }
 
@@ -343,7 +344,7 @@ int moe_grouped_fc2(const moe_handle* h, int32_t F, int32_t wdtype, const void* 
     int ncu = 0;
     int rc = check_mlp(h, F, wdtype, d_w2, d_w2_scales, d_scratch, scratch_bytes, &ncu);
     if (rc) return rc;
-    if (!d_expert_out) return MOE_EINVAL;
+    if (h->desc.out_rows > 0 && !d_expert_out) return MOE_EINVAL;
     if (!al16(d_expert_out)) return MOE_EALIGN;
     if (wdtype == MOE_FP8E4M3_B128)
         return hip_rc(launch_gemm_fp8(h, 1, F, nullptr, nullptr, d_w2, d_w2_scales, d_scratch, d_expert_out,
@@ -360,7 +361,7 @@ int moe_grouped_fc2_fp8out(const moe_handle* h, int32_t F, int32_t wdtype, const
     int rc = check_mlp(h, F, wdtype, d_w2, d_w2_scales, d_scratch, scratch_bytes, &ncu);
     if (rc) return rc;
     if (wdtype != MOE_BF16) return MOE_EUNSUPPORTED;
-    if (!d_out_q || !d_out_scales) return MOE_EINVAL;
+    if (h->desc.out_rows > 0 && (!d_out_q || !d_out_scales)) return MOE_EINVAL;
     if (!al16(d_out_q) || !al4(d_out_scales)) return MOE_EALIGN;
     return hip_rc(launch_gemm_bf16(h, 1, F, d_scratch, d_w2, d_out_q, d_out_scales, ncu, (hipStream_t)stream));
 }

@@ -224,7 +224,8 @@ int moe_dispatch(moe_handle* h, const void* d_routing, const float* d_probs,
  * MOE_FP8E4M3_B128 holds the fp32 FC1 activations plus the e4m3 codes and
  * fp32 1x128 scales of the permuted rows and of the activations (each input
  * is quantised once per call); MOE_INT4_G128 holds bf16 activations
- * in the feature order that its FC2 reads.  0 if invalid. */
+ * in the feature order that its FC2 reads.  0 if invalid, never 0 for a valid
+ * shape: with R = 0 the MLP calls take null rows and launch nothing. */
 size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype);
 
 /* Grouped expert MLP over the permuted rows: for every expert e and every

@@ -40,3 +40,21 @@ def test_scales_off_a_16_byte_line(T, E, K, H, F, floats):
     d.grouped_mlp(perm, c1, c2, w1_scales=s1, w2_scales=s2, out=same)
     torch.cuda.synchronize()
     assert torch.equal(same, out)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_empty_batch_through_the_layer(score):
+    """No tokens: the MLP alone and the whole layer with norm and gate return
+    empty outputs."""
+    E, K, H, F = 4, 2, 256, 128
+    d = Dispatcher(0, H, E, K, route_fmt="dense_i32", device=DEV)
+    assert d.R == 0
+    c1, s1, c2, s2 = (t.to(DEV) for t in _weights(E, 2 * F, H, 2) + _weights(E, H, F, 3))
+    x, wr = torch.empty((0, H), dtype=BF, device=DEV), torch.zeros((E, H), device=DEV)
+    kw = dict(w1_scales=s1, w2_scales=s2, norm=(torch.ones(H, device=DEV), None),
+              router=lambda rows: rows.float() @ wr.T, gate=dict(score=score))
+    perm, *_ = d.dispatch(x, torch.empty((0, K), dtype=torch.int32, device=DEV))
+    assert tuple(d.grouped_mlp(perm, c1, c2, w1_scales=s1, w2_scales=s2).shape) == (0, H)
+    assert tuple(d.layer(x, None, None, c1, c2, **kw).shape) == (0, H)
+    torch.cuda.synchronize()
+    assert d.tokens_per_expert.cpu().tolist() == [0] * E
