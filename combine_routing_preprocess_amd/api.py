@@ -29,6 +29,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()      # c_void_p arguments take addresses as they are
 
 
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
 def _stream():
     # the current stream's handle, without building a Stream object (2.9 us of a call that launches in 4)
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -157,14 +161,14 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=x.device)
         _need(scratch.is_contiguous(), "scratch must be contiguous")
-        if scratch.numel() * scratch.element_size() < need:
+        if _nbytes(scratch) < need:
             raise ValueError(f"scratch holds fewer than the {need} bytes needed")
     else:
         _need(grad_weight is None and grad_bias is None, "grad_weight and grad_bias need want_params")
     _check_current_device((("grad_y", grad_y), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight),
                            ("out", out), ("grad_weight", grad_weight), ("grad_bias", grad_bias),
                            ("scratch", scratch)))
-    nbytes = 0 if scratch is None else scratch.numel() * scratch.element_size()
+    nbytes = 0 if scratch is None else _nbytes(scratch)
     A.check(A.lib().moe_layer_norm_backward(T, H, _ROW_DT[x.dtype], _ROW_DT[grad_y.dtype], wdt, _ptr(grad_y), _ptr(x),
                                             _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(out), _ptr(grad_weight),
                                             _ptr(grad_bias), _ptr(scratch), nbytes, _stream()),
@@ -471,7 +475,7 @@ class Dispatcher:
             need = self._scratch_need[F, wdtype] = self.mlp_scratch_bytes(F, wdtype)
         if need <= 0:
             raise ValueError(f"invalid FFN width {F} for {wdtype} weights")
-        if scratch.numel() * scratch.element_size() < need:
+        if _nbytes(scratch) < need:
             raise ValueError(f"scratch holds fewer than the {need} bytes needed")
 
     def _check_expert_out(self, out: torch.Tensor):
@@ -503,7 +507,7 @@ class Dispatcher:
             _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_swiglu_mlp(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(scratch),
-                                               scratch.numel() * scratch.element_size(), _ptr(out), _stream()),
+                                               _nbytes(scratch), _ptr(out), _stream()),
                 "moe_grouped_swiglu_mlp")
         return out
 
@@ -537,7 +541,7 @@ class Dispatcher:
         if wdtype == "int4":
             _check_current_device((("perm", perm),))
         A.check(A.lib().moe_grouped_fc1_swiglu(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
-                                               _ptr(w1_scales), _ptr(scratch), scratch.numel(), _stream()),
+                                               _ptr(w1_scales), _ptr(scratch), _nbytes(scratch), _stream()),
                 "moe_grouped_fc1_swiglu")
         self._fc1_done = (F, wdtype, scratch.data_ptr())
 
@@ -558,7 +562,7 @@ class Dispatcher:
         if wdtype == "int4":
             _check_current_device((("out", out),))
         A.check(A.lib().moe_grouped_fc2(C.byref(self.h), F, _DT[wdtype], _ptr(w2), _ptr(w2_scales), _ptr(scratch),
-                                        scratch.numel(), _ptr(out), _stream()), "moe_grouped_fc2")
+                                        _nbytes(scratch), _ptr(out), _stream()), "moe_grouped_fc2")
         return out
 
     def fc2_fp8out(self, w2: torch.Tensor, scratch: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -579,7 +583,7 @@ class Dispatcher:
         _need(out_scales.dtype == torch.float32 and tuple(out_scales.shape) == (self.R, self.H // 128),
               "out_scales must be float32 [R, H/128]")
         A.check(A.lib().moe_grouped_fc2_fp8out(C.byref(self.h), F, A.BF16, _ptr(w2), None, _ptr(scratch),
-                                               scratch.numel(), _ptr(out), _ptr(out_scales), _stream()),
+                                               _nbytes(scratch), _ptr(out), _ptr(out_scales), _stream()),
                 "moe_grouped_fc2_fp8out")
         return out, out_scales
 
@@ -690,7 +694,7 @@ class Dispatcher:
         _need(wdtype == "fp8" and wdtype2 == "fp8" and F2 == F, "the decode layer takes fp8 w1 and w2 of one FFN width")
         self._dev(scratch, "scratch")
         need = self.decode_layer_scratch_bytes(F)
-        _need(need > 0 and scratch.numel() * scratch.element_size() >= need,
+        _need(need > 0 and _nbytes(scratch) >= need,
               f"scratch holds fewer than the {need} bytes needed")
         self._check_expert_out(expert_out)
         self._dev(out, "out")
@@ -698,7 +702,7 @@ class Dispatcher:
         self._dev(status, "status")
         _need(status.dtype == torch.int32 and status.numel() == 1, "status must be one int32")
         A.check(A.lib().moe_decode_layer_fp8(C.byref(self.h), F, _ptr(x), _ptr(w1), _ptr(w1_scales), _ptr(w2),
-                                             _ptr(w2_scales), _ptr(scratch), scratch.numel(), _ptr(expert_out),
+                                             _ptr(w2_scales), _ptr(scratch), _nbytes(scratch), _ptr(expert_out),
                                              1 if apply_probs else 0, _ptr(out), _ptr(status), _stream()),
                 "moe_decode_layer_fp8")
         return out
@@ -721,12 +725,12 @@ class Dispatcher:
         self._dev(scratch, "scratch")
         need = self.decode_fused_scratch_bytes(F)
         _need(need > 0, "the fused decode layer needs H, F multiples of 128 and H <= 8192")
-        _need(scratch.numel() * scratch.element_size() >= need, f"scratch holds fewer than the {need} bytes needed")
+        _need(_nbytes(scratch) >= need, f"scratch holds fewer than the {need} bytes needed")
         self._check_expert_out(expert_out)
         self._dev(out, "out")
         _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (self.T, self.H), "out must be bf16 [T,H]")
         A.check(A.lib().moe_decode_fused_fp8(C.byref(self.h), F, _ptr(x), _ptr(w1), _ptr(w1_scales), _ptr(w2),
-                                             _ptr(w2_scales), _ptr(scratch), scratch.numel() * scratch.element_size(),
+                                             _ptr(w2_scales), _ptr(scratch), _nbytes(scratch),
                                              _ptr(expert_out), 1 if apply_probs else 0, _ptr(out), _stream()),
                 "moe_decode_fused_fp8")
         return out
