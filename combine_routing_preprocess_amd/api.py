@@ -239,6 +239,10 @@ class Dispatcher:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
+    def _check_here(self):
+        # the workspace on the current GPU leaves _dev the current GPU alone to accept
+        _check_current_device((("the Dispatcher's workspace", self.ws),))
+
     def _check_routing(self, routing, probs, T_live):
         self._dev(routing, "routing")
         if routing.dtype not in _FMT_DTYPES[self.route_fmt]:
@@ -504,7 +508,7 @@ class Dispatcher:
             out = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device((("perm", perm),))
+            self._check_here()
         A.check(A.lib().moe_grouped_swiglu_mlp(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                                _nbytes(scratch), _ptr(out), _stream()),
@@ -524,7 +528,7 @@ class Dispatcher:
         self._check_perm(perm, perm_scales)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device((("perm", perm),))
+            self._check_here()
         A.check(A.lib().moe_grouped_swiglu_mlp_noalloc(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales),
                                                        _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(out),
                                                        _stream()), "moe_grouped_swiglu_mlp_noalloc")
@@ -539,7 +543,7 @@ class Dispatcher:
         self._check_perm(perm, perm_scales)
         self._check_scratch(scratch, F, wdtype)
         if wdtype == "int4":
-            _check_current_device((("perm", perm),))
+            self._check_here()
         A.check(A.lib().moe_grouped_fc1_swiglu(C.byref(self.h), F, _DT[wdtype], _ptr(perm), _ptr(perm_scales), _ptr(w1),
                                                _ptr(w1_scales), _ptr(scratch), _nbytes(scratch), _stream()),
                 "moe_grouped_fc1_swiglu")
@@ -560,7 +564,7 @@ class Dispatcher:
         self._check_after_fc1(F, wdtype, scratch)
         self._check_expert_out(out)
         if wdtype == "int4":
-            _check_current_device((("out", out),))
+            self._check_here()
         A.check(A.lib().moe_grouped_fc2(C.byref(self.h), F, _DT[wdtype], _ptr(w2), _ptr(w2_scales), _ptr(scratch),
                                         _nbytes(scratch), _ptr(out), _stream()), "moe_grouped_fc2")
         return out
