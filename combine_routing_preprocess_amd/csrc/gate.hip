@@ -38,7 +38,8 @@ namespace {
 using namespace ops;
 
 constexpr double kOut = -INFINITY;   // logit or key of an expert that is no candidate
-constexpr double kTiny = 1e-280;     // sums of sigmoids below this are formed from logarithms
+constexpr double kTiny = 1e-260;     // sums of sigmoids below this are formed from logarithms, so that the largest
+                                     // scale over a sum (3.4e38 / 1e-260) stays a 64-bit number
 
 // exp(x) for x <= 0 (0 for NaN): x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in
 // two parts), the Taylor polynomial of degree 13 at r (next term 4e-18),
