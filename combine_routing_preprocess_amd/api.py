@@ -295,7 +295,8 @@ class Dispatcher:
                       score: str = "softmax", normalize: bool = False, scale: float = 1.0,
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Gradient of the gate's weights (grad_probs, in the routing's shape,
-        as combine_backward gives it) to the logits [T,E], in their dtype."""
+        as combine_backward gives it) to the logits [T,E], in their dtype.
+        ``out`` may be the logits."""
         self._check_gate(logits, score)
         shape = self._routing_shape()
         _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])

@@ -502,6 +502,18 @@ namespace {
 
 bool row_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_F32; }
 
+size_t row_bytes(int32_t T, int32_t H, int32_t dtype) { return (size_t)T * H * (dtype == MOE_BF16 ? 2 : 4); }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return p < q + nb && q < p + na;
+}
+
+// Elements of an array in the routing's shape.
+size_t routed_floats(const moe_desc& d) {
+    return (size_t)d.T * (d.route_fmt == MOE_ROUTE_SPARSE_BOOL ? d.E : d.K);
+}
+
 // Checks shared by the gate and its backward pass: score, type and the three
 // arrays in the shapes of logits and routing.
 int check_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, int32_t score, float scale,
@@ -521,13 +533,6 @@ int check_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dtype, int32_t w
     return row_dtype(x_dtype) && row_dtype(y_dtype) && row_dtype(w_dtype) ? MOE_OK : MOE_EDTYPE;
 }
 
-size_t row_bytes(int32_t T, int32_t H, int32_t dtype) { return (size_t)T * H * (dtype == MOE_BF16 ? 2 : 4); }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
-    return p < q + nb && q < p + na;
-}
-
 }  // namespace
 
 int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, const float* d_bias, int32_t score,
@@ -535,6 +540,13 @@ int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, con
     int rc = check_gate(h, d_logits, logit_dtype, score, scale, d_routing, d_probs);
     if (rc) return rc;
     if (d_bias && !al4(d_bias)) return MOE_EALIGN;
+    const moe_desc& d = h->desc;
+    const size_t nl = row_bytes(d.T, d.E, logit_dtype), nr = (size_t)moe_routing_bytes(&d);
+    const size_t np = routed_floats(d) * 4, nb = d_bias ? (size_t)d.E * 4 : 0;
+    if (d.T > 0 && (overlap(d_routing, nr, d_logits, nl) || overlap(d_probs, np, d_logits, nl) ||
+                    overlap(d_routing, nr, d_probs, np) || overlap(d_routing, nr, d_bias, nb) ||
+                    overlap(d_probs, np, d_bias, nb)))
+        return MOE_EINVAL;
     return hip_rc(launch_gate(h, d_logits, logit_dtype, d_bias, score == MOE_GATE_SIGMOID, normalize ? 1 : 0, scale,
                               d_routing, d_probs, (hipStream_t)stream));
 }
@@ -546,6 +558,12 @@ int moe_gate_backward(const moe_handle* h, const float* d_grad_probs, const void
     if (rc) return rc;
     if (h->desc.T > 0 && !d_grad_logits) return MOE_EINVAL;
     if (!al16(d_grad_logits)) return MOE_EALIGN;
+    const moe_desc& d = h->desc;
+    const size_t nl = row_bytes(d.T, d.E, logit_dtype);
+    if (d.T > 0 && ((d_grad_logits != d_logits && overlap(d_grad_logits, nl, d_logits, nl)) ||
+                    overlap(d_grad_logits, nl, d_grad_probs, routed_floats(d) * 4) ||
+                    overlap(d_grad_logits, nl, d_routing, (size_t)moe_routing_bytes(&d))))
+        return MOE_EINVAL;
     return hip_rc(launch_gate_backward(h, d_grad_probs, d_logits, logit_dtype, d_routing, score == MOE_GATE_SIGMOID,
                                        normalize ? 1 : 0, scale, d_grad_logits, (hipStream_t)stream));
 }

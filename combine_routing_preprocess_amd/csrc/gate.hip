@@ -323,13 +323,16 @@ __device__ __forceinline__ void store_grad(LT* p, double v) {
     else *p = (float)v;
 }
 
+// Both backward kernels read all they need of a row before they write it: the
+// gradient may take the logits' place.
+//
 // Dense routing, K <= 64: lane j has slot j.  Only the chosen experts' logits
 // are read, but for the softmax over the whole row.
 template <typename LT, typename IT, int EPL>
 __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__ grad_probs,
-                                                       const LT* __restrict__ logits, const IT* __restrict__ routing,
-                                                       int T, int E, int K, int sigmoid, int normalize, float scale,
-                                                       LT* __restrict__ grad_logits) {
+                                                       const LT* logits, const IT* __restrict__ routing, int T, int E,
+                                                       int K, int sigmoid, int normalize, float scale,
+                                                       LT* grad_logits) {
     const int lane = threadIdx.x & 63;
     const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
@@ -386,10 +389,9 @@ __global__ __launch_bounds__(256) void k_gate_backward(const float* __restrict__
 // Boolean map, or any K: slots counted at the experts' lanes.
 template <typename LT, int FMT, int EPL>
 __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restrict__ grad_probs,
-                                                            const LT* __restrict__ logits,
-                                                            const void* __restrict__ routing, int T, int E, int K,
-                                                            int sigmoid, int normalize, float scale,
-                                                            LT* __restrict__ grad_logits) {
+                                                            const LT* logits, const void* __restrict__ routing, int T,
+                                                            int E, int K, int sigmoid, int normalize, float scale,
+                                                            LT* grad_logits) {
     const int lane = threadIdx.x & 63;
     const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;

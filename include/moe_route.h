@@ -465,7 +465,8 @@ int moe_combine_backward(const moe_handle* h, const void* d_grad_y, const void* 
  *   d_logits     [T,E]
  *   d_bias       nullable [E] fp32; steers the choice only
  *   d_routing    out, [T,K] int16 / int32 or [T,E] uint8 (0 / 1)
- *   d_probs      out, fp32 in the routing's shape; 0 where nothing is chosen */
+ *   d_probs      out, fp32 in the routing's shape; 0 where nothing is chosen
+ * The outputs must overlap neither the inputs nor each other (MOE_EINVAL). */
 enum moe_gate_score { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
 int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, const float* d_bias, int32_t score,
              int32_t normalize, float scale, void* d_routing, float* d_probs, void* stream);
@@ -479,7 +480,9 @@ int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, con
  *   d_grad_probs   fp32 in the routing's shape
  *   d_logits       [T,E] the forward's logits
  *   d_routing      the forward's routing
- *   d_grad_logits  [T,E] out, of logit_dtype */
+ *   d_grad_logits  [T,E] out, of logit_dtype; may be d_logits (then the logits
+ *                  are overwritten), no other overlap with the inputs
+ *                  (MOE_EINVAL) */
 int moe_gate_backward(const moe_handle* h, const float* d_grad_probs, const void* d_logits, int32_t logit_dtype,
                       const void* d_routing, int32_t score, int32_t normalize, float scale, void* d_grad_logits,
                       void* stream);

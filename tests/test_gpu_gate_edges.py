@@ -27,3 +27,24 @@ def test_large_scale_over_a_small_sum(E, K, fmt, dtype):
     scale = float(torch.tensor(3e38, dtype=F32))
     idx, w = _oracle(z.double().numpy(), K, None, "sigmoid", True, scale)
     _compare(d, fmt, routing, probs, idx, w, E)
+
+
+@pytest.mark.parametrize("fmt", ["dense_i16", "sparse_bool"])
+@pytest.mark.parametrize("E,K", [(60, 4), (256, 8), (160, 96), (1000, 6)])
+@pytest.mark.parametrize("score,normalize", [("softmax", False), ("softmax", True), ("sigmoid", False),
+                                             ("sigmoid", True)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gradient_in_the_logits_place(E, K, fmt, score, normalize, dtype):
+    """The same bits as into a tensor of its own."""
+    log("gate backward in place", E, K, fmt, score, normalize, dtype)
+    T = 70
+    gen = torch.Generator().manual_seed(E + K)
+    z = (2 * torch.randn(T, E, generator=gen)).to(dtype).to(DEV)
+    d = Dispatcher(T, 64, E, K, route_fmt=fmt, device=DEV)
+    kw = dict(score=score, normalize=normalize, scale=2.5)
+    routing, probs = d.gate(z, **kw)
+    g = torch.randn(probs.shape, generator=gen).to(DEV)
+    want = d.gate_backward(g, z, routing, **kw)
+    got = d.gate_backward(g, z, routing, out=z, **kw)
+    torch.cuda.synchronize()
+    assert got is z and torch.equal(got, want)
