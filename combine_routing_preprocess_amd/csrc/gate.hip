@@ -437,8 +437,10 @@ __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restr
         }
     }
     // p = scores (or the chosen scores' shares), dot = sum over the slots of G p
+    const bool whole = !sigmoid && !normalize;
+    auto has_share = [&](int i) { return whole ? l[i] != -INFINITY : cnt[i] > 0; };
     double m = 0.0, sum = 1.0, p[EPL], rest[EPL], part = 0.0;
-    if (!sigmoid && !normalize) {
+    if (whole) {
         softmax_terms<EPL>(l, &m, &sum);
     } else if (!sigmoid) {
         m = kOut;
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restr
     for (int i = 0; i < EPL; ++i) {
         p[i] = 0.0;
         rest[i] = 1.0;
-        if (l[i] != -INFINITY && (cnt[i] || (!sigmoid && !normalize))) {
+        if (has_share(i)) {
             if (sigmoid) sigmoids((double)l[i], &p[i], &rest[i]);
             else p[i] = exp_neg((double)l[i] - m);
         }
@@ -479,7 +481,7 @@ __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restr
     double dot = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = p[i] != 0.0 ? p[i] / sum : 0.0;   // exactly 1 where it is all of the sum
+        p[i] = has_share(i) ? p[i] / sum : 0.0;   // exactly 1 where it is all of the sum; NaN in the row of a +inf
         dot += g[i] * p[i];
     }
     dot = !sigmoid || normalize ? wave_sum_dpp(dot) : 0.0;
@@ -490,7 +492,7 @@ __global__ __launch_bounds__(256) void k_gate_backward_many(const float* __restr
         // a slot's own gradient less, through the sum that divides it, the dot:
         // with the chosen scores' sum each slot of the expert carries it once
         const double o = p[i] * rest[i] * (g[i] - (normalize ? cnt[i] : 1) * dot) * (double)scale;
-        store_grad(grad_logits + t * E + e, p[i] != 0.0 ? o : 0.0);
+        store_grad(grad_logits + t * E + e, has_share(i) ? o : 0.0);
     }
 }
 

@@ -476,6 +476,7 @@ int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, con
  * with the choice held fixed (the bias has no gradient).  Entries of empty
  * slots (an index outside [0, E)), of unrouted experts and of experts whose
  * logit is NaN or -inf are ignored; a repeated index counts once per slot.
+ * In the row of a +inf logit the softmax's gradients are NaN, as its weights.
  * Every element of d_grad_logits is written.
  *   d_grad_probs   fp32 in the routing's shape
  *   d_logits       [T,E] the forward's logits

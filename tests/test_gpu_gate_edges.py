@@ -48,3 +48,40 @@ def test_gradient_in_the_logits_place(E, K, fmt, score, normalize, dtype):
     got = d.gate_backward(g, z, routing, out=z, **kw)
     torch.cuda.synchronize()
     assert got is z and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt,E,K", [("dense_i32", 12, 3), ("sparse_bool", 12, 3), ("sparse_bool", 300, 8),
+                                     ("dense_i32", 160, 96)])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_gradient_of_infinite_logits(fmt, E, K, normalize):
+    """Softmax weights of a row with a +inf logit are NaN, and so are their
+    gradients in every routing format: of the whole row, or with `normalize`
+    of the chosen experts.  The rows beside it stay finite, and a sigmoid's
+    gradient at +inf is 0."""
+    log("gate backward infinite", fmt, E, K, normalize)
+    T = 6
+    gen = torch.Generator().manual_seed(E + 7 * K)
+    z = torch.randn(T, E, generator=gen)
+    z[2, 5] = float("inf")
+    z[2, 1] = float("-inf")
+    z[4, 2], z[4, 3] = float("inf"), float("inf")
+    zd = z.to(DEV)
+    d = Dispatcher(T, 64, E, K, route_fmt=fmt, device=DEV)
+    for score in ("softmax", "sigmoid"):
+        routing, probs = d.gate(zd, score=score, normalize=normalize)
+        g = torch.randn(probs.shape, generator=gen).to(DEV)
+        got = d.gate_backward(g, zd, routing, score=score, normalize=normalize).cpu()
+        if fmt == "sparse_bool":
+            chosen = routing.cpu().bool()
+        else:
+            chosen = torch.zeros(T, E, dtype=torch.bool).scatter_(1, routing.cpu().long(), True)
+        assert bool(chosen[2, 5]) and bool(chosen[4, 2:4].all())
+        others = [0, 1, 3, 5]
+        assert bool(torch.isfinite(got[others]).all())
+        if score == "sigmoid":
+            assert bool(torch.isfinite(got).all()) and float(got[2, 5]) == 0.0
+            continue
+        for t in (2, 4):
+            through = chosen[t] if normalize else z[t] != float("-inf")
+            assert bool(torch.isnan(got[t][through]).all()), t
+            assert bool((got[t][~through] == 0).all()), t
