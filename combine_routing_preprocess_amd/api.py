@@ -105,7 +105,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None):
     """Layer norm of rows x [T,H] (bf16 or fp32; weight and bias [H] of one of
     these types): (out [T,H], mean [T], rstd [T]), the last two fp32, for
-    layer_norm_backward.  ``out`` is of ``out_dtype`` (default: x's)."""
+    layer_norm_backward.  ``out`` is of ``out_dtype`` (default: x's).  Rows,
+    weight and bias start at a multiple of 16 bytes, rows of any width follow
+    each other without gaps."""
     _need(x.dim() == 2, "x must be [T,H]")
     T, H = x.shape
     _check_rows(x, "x", (T, H), _ROW_DT)
@@ -272,7 +274,8 @@ class Dispatcher:
         """The top-k experts of each token and their weights from router logits
         [T,E] (bf16 or fp32): (routing, probs) in this Dispatcher's routing
         format, as preprocess and dispatch take them.  ``bias`` [E] (fp32)
-        steers the choice only; -inf logits switch experts off."""
+        steers the choice only; -inf logits switch experts off.  Logits and
+        routing start at a multiple of 16 bytes."""
         self._check_gate(logits, score)
         if bias is not None:
             _check_rows(bias, "bias", (self.E,), _F32)

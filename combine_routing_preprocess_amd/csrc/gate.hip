@@ -27,9 +27,12 @@
 //  * exp and the reciprocal below are for arguments that occur here (x <= 0
 //    and 1 <= d <= 2) and take some 20 and 6 instructions instead of the
 //    library's general forms.
-//  * Measured on MI355X, 256 experts top-8 with bias: 8192 tokens in 11.1 us
-//    (the logits alone would take 1.7 us; with shuffles through LDS and the
-//    library's exp 26 us), 16 tokens in 4.8 us; gradient of 8192 tokens 8.9 us.
+//  * Measured on MI355X, 256 experts top-8 with bias, in long runs of calls:
+//    8192 tokens in 9.6 us, 11.1 in a run of a dozen (the logits alone would
+//    take 1.7 us; with shuffles through LDS and the library's exp 26 us), 16
+//    tokens in 4.4 us; gradient of 8192 tokens 7.9 us, of a Boolean map 10 us
+//    (softmax over the row 13).  More than 64 slots: 8192 tokens, 160 experts
+//    top-96 in 49 us, their gradient in 48.
 #include "wave_ops.h"
 
 namespace moe {

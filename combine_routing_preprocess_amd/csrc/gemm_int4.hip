@@ -17,9 +17,9 @@
 //    Weights and scales are the wavefront's own, tokens are shared (passes of
 //    up to four rows have a copy per wavefront and no barriers).  Without the
 //    arithmetic the transfers alone run at 6.8 TB/s.
-//  * The loop is balanced between those transfers and some 160 vector and 24
-//    matrix instructions per step and wavefront, so that many steps have to
-//    overlap on a CU: three workgroups of two ring slots each (64 tokens, 256
+//  * The loop is balanced between those transfers and some 190 vector (FC2:
+//    157) and 24 matrix instructions per step and wavefront, so that many steps
+//    have to overlap on a CU: three workgroups of two ring slots each (64 tokens, 256
 //    experts top-8, 7168 x 2048: 876 us, against 914 with two workgroups of
 //    three slots).  Where a CU gets one or two units the ring is deeper, and
 //    two sets of wavefronts take every other step of a lone unit (one token:
@@ -441,7 +441,10 @@ hipError_t launch_gemm_int4(const moe_handle* h, int stage, int F, const void* i
     // The largest pass that still gives nearly every CU a workgroup: rows that share a dequantised weight against
     // CUs at work.  500 tokens, 24 experts of 1152 x 640 (240 units of 64 rows): 38.0 us with 64, 42.1 with 32; 100
     // tokens, 16 experts of 3584 x 512 (64 units of 64 rows, 256 of 32): 61.9 and 39.1, with 16 rows 44.1; 128 tokens,
-    // 4 experts of 512 x 256 (16, 64 and 128 units): 19.4, 10.8 and 8.8.
+    // 4 experts of 512 x 256 (16, 64 and 128 units): 19.4, 10.8 and 8.8.  In between, 2048 x 1024 with 128 units of 64
+    // rows: 63.0 us against 41.6 with fewer rows a pass, 160: 50.0 and 55.1, 192: 51.5 and 58.2 (4096 x 2048 with 67
+    // rows an expert, which 32 cut better: 84.0 and 68.7), 208: 70.4 and 70.5, 256: 77.2 and 83.2.  Seven eighths of the
+    // CUs keep clear of the side that loses a third.
     auto workgroups = [&](int rows, int waves) { return (long long)experts * upe(waves) * ((avg + rows - 1) / rows); };
     const long long most = workgroups(16, 4);
     if (avg > kWide && 8 * workgroups(64, 8) >= 7ll * num_cu) go(r64, two, one, eight);

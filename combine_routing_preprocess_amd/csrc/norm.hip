@@ -12,11 +12,12 @@
 // rows share a workgroup when they are short.  Workgroups walk the rows with a
 // stride, so weight and bias are loaded once per workgroup, and the loads of
 // the next two rows are in flight during the current row's reductions.
-// Measured on MI355X, 8192 x 7168 bf16: forward 45.7 us (5.1 TB/s), backward
-// 72 us and the sum of its parameter gradients 5 us (together 4.7 TB/s), where
-// a 1 GiB device copy runs at 5.08 TB/s.  The forward takes 2 chunks per lane
-// (7 wavefronts per row; 14 of one chunk: 61 us), the backward one, for the
-// column sums that each lane keeps (two chunks spill: 126 us).
+// Measured on MI355X, 8192 x 7168 bf16, in long runs of calls: forward 47.0 us
+// (5.0 TB/s), backward with the sum of its parameter gradients 73.8 us (4.8
+// TB/s), where a 1 GiB device copy runs at 5.08 TB/s.  The forward takes 2
+// chunks per lane there (7 wavefronts per row), the backward one, for the
+// column sums that each lane keeps (two chunks spill: 126 us; so do the two
+// and four of wider rows, 57 M elements as 16384 columns in 158 us).
 //
 // Statistics are fp32 and need one barrier per row.  Each wavefront takes the
 // mean m of its own part, then the sum e and the square sum q of what is left,
@@ -456,10 +457,18 @@ __global__ __launch_bounds__(256) void k_norm_param_grads(const float* __restric
 
 constexpr int kMaxRowElems = 64 * 8 * kMaxWaves * 4;   // 4 steps of 16 wavefronts
 static_assert(kMaxRowElems == MOE_NORM_MAX_H, "norm row limit");
-constexpr int kBackwardBlocks = 256;                   // one workgroup per CU walks the rows
+// One workgroup per CU of the whole chip walks the rows, whatever part of it the call runs on: the scratch's size is a
+// function of the shape alone.  8192 x 7168 bf16: 72.8 us, 80.6 with 512 and 115.7 with 128; 114688 x 512: 68.9,
+// 75.7 and 88.0.
+constexpr int kBackwardBlocks = 256;
 
 // Steps per lane and wavefronts per row: at most `wide` wavefronts share a row
-// while 2 steps do.
+// while 2 steps do.  The forward's 8 against 16 and 4, 57 M bf16 elements again
+// and again: 2560 columns 49.2 us (16: 48.0, 4: 42.1), 4096 45.8 (45.1, 41.5),
+// 4608 47.7 (47.4, 48.1), 5120 45.7 (58.4, 45.4), 6144 46.8 (45.5, 47.1), 7168
+// 41.2 (46.7, 40.4), 8192 40.2 (44.3, 40.4); 256 rows of 2560 3.3 us (4: 3.6),
+// of 4096 3.5 (3.8).  16 loses from 5120 columns on; 4 wins 10 to 14 % in large
+// batches of 2560 to 4096 columns and loses 8 % in small ones, where 8 stays.
 void row_shape(int H, int wide, int* NC, int* W) {
     const int groups = (H + 511) / 512;   // 64-lane groups of chunks
     *NC = groups <= wide ? 1 : groups <= 2 * kMaxWaves ? 2 : 4;
@@ -511,8 +520,10 @@ hipError_t launch_layer_norm(int T, int H, int x_dtype, int y_dtype, int w_dtype
     row_shape(H, kForwardWide, &NC, &W);
     const int G = W >= 4 ? 1 : 4 / W;
     const int per_cu = max(1, 32 / (W * G));
-    // outputs past the 32 MB of L2 leave it anyway: nontemporal stores, 8192 x 7168 bf16 in 43.6 us against 55.8
-    // (5.4 and 4.2 TB/s); smaller ones stay for the router's product and the dispatch that read them next
+    // Outputs past the 32 MB of L2 leave it anyway: nontemporal stores; smaller ones stay for the router's product and
+    // the dispatch that read them next.  8192 x 7168 bf16 with and without, and with who reads the rows: alone 51.3 and
+    // 55.0 us, with the router's product 136.4 and 135.5, with the dispatch 248 and 240 (the rows stay in the last-level
+    // cache), with product, gate, routing and dispatch as the layer runs them 337 and 340
     const bool stream = (long long)T * H * (y_dtype == MOE_BF16 ? 2 : 4) > (32ll << 20);
     const long long want = ((long long)T + G - 1) / G, most = (long long)num_cu * per_cu;
     const unsigned grid = (unsigned)(want < most ? want : most);

@@ -249,7 +249,8 @@ size_t moe_mlp_scratch_bytes(const moe_handle* h, int32_t F, int32_t wdtype);
  *          before FC2; requires H, F multiples of 128.  Built for decode-sized
  *          batches (few rows per expert; weight streaming bound).
  *   wdtype MOE_INT4_G128: d_w1 [E,2F,H/2] codes, d_w1_scales [E,2F,H/128]
- *          fp32, d_w2 [E,H,F/2] codes, d_w2_scales [E,H,F/128] fp32; the rows
+ *          fp32, d_w2 [E,H,F/2] codes, d_w2_scales [E,H,F/128] fp32 (scales
+ *          4-byte aligned, moved fastest from a multiple of 16); the rows
  *          stay bf16 (bf16 payload only), products and scales are fp32, a is
  *          rounded once to bf16 before FC2 as with bf16 weights; requires H,
  *          F multiples of 128.  Rows that hold no kept copy are not written.
@@ -462,7 +463,7 @@ int moe_combine_backward(const moe_handle* h, const void* d_grad_y, const void* 
  * A +inf logit is chosen first; its row's softmax weights are NaN, and with a
  * bias its row's softmax keys are, so that the row is unrouted.
  *   logit_dtype  MOE_BF16 or MOE_F32 (else MOE_EDTYPE)
- *   d_logits     [T,E]
+ *   d_logits     [T,E], 16-byte aligned as d_routing
  *   d_bias       nullable [E] fp32; steers the choice only
  *   d_routing    out, [T,K] int16 / int32 or [T,E] uint8 (0 / 1)
  *   d_probs      out, fp32 in the routing's shape; 0 where nothing is chosen
@@ -479,7 +480,8 @@ int moe_gate(const moe_handle* h, const void* d_logits, int32_t logit_dtype, con
  * In the row of a +inf logit the softmax's gradients are NaN, as its weights.
  * Every element of d_grad_logits is written.
  *   d_grad_probs   fp32 in the routing's shape
- *   d_logits       [T,E] the forward's logits
+ *   d_logits       [T,E] the forward's logits, 16-byte aligned as d_routing
+ *                  and d_grad_logits
  *   d_routing      the forward's routing
  *   d_grad_logits  [T,E] out, of logit_dtype; may be d_logits (then the logits
  *                  are overwritten), no other overlap with the inputs
