@@ -18,6 +18,7 @@ ROUTE_DENSE_I16, ROUTE_DENSE_I32, ROUTE_SPARSE_BOOL = 0, 1, 2
 BF16, FP8E4M3_B128, F32, INT4_G128 = 0, 1, 2, 3
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 NORM_MAX_H = 32768
+GROUPED_MAX = 65536
 
 FLAG_CAPACITY, FLAG_OUT_ROWS, FLAG_BAD_EXPERT, FLAG_DUPLICATE = 1, 2, 4, 8
 
@@ -87,6 +88,15 @@ SIGNATURES = [
     ("moe_layer_norm", C.c_int, [C.c_int32] * 5 + [_P, _P, _P, C.c_float, _P, _P, _P, _P]),
     ("moe_layer_norm_backward_scratch_bytes", C.c_size_t, [C.c_int32, C.c_int32]),
     ("moe_layer_norm_backward", C.c_int, [C.c_int32] * 5 + [_P] * 9 + [C.c_size_t, _P]),
+    ("moe_grouped_product", C.c_int, [C.POINTER(MoeHandle), C.c_int32, C.c_int32, C.c_int32, _P, _P, _P, _P]),
+    ("moe_grouped_weight_grad", C.c_int, [C.POINTER(MoeHandle)] + [C.c_int32] * 4 + [_P, _P, _P, _P]),
+    ("moe_grouped_mlp_keep", C.c_int, [C.POINTER(MoeHandle), C.c_int32, _P, _P, _P, _P, C.c_size_t, _P, _P, _P]),
+    ("moe_mlp_backward_scratch_bytes", C.c_size_t, [C.POINTER(MoeHandle), C.c_int32]),
+    ("moe_grouped_mlp_backward", C.c_int, [C.POINTER(MoeHandle)] + [C.c_int32] * 3 + [_P] * 6 + [C.c_size_t] +
+                                          [_P] * 4),
+    ("moe_rms_norm", C.c_int, [C.c_int32] * 6 + [_P, _P, _P, C.c_float] + [_P] * 6),
+    ("moe_rms_norm_backward_scratch_bytes", C.c_size_t, [C.c_int32, C.c_int32]),
+    ("moe_rms_norm_backward", C.c_int, [C.c_int32] * 5 + [_P] * 8 + [C.c_size_t, _P]),
 ]
 
 _lib = None

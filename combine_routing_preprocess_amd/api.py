@@ -8,7 +8,7 @@ device value back to the host.
 from __future__ import annotations
 
 import ctypes as C
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -20,6 +20,7 @@ _FMT_DTYPES = {A.ROUTE_DENSE_I16: (torch.int16,), A.ROUTE_DENSE_I32: (torch.int3
 _DT = {"bf16": A.BF16, "fp8": A.FP8E4M3_B128, "int4": A.INT4_G128}
 _ROW_DT = {torch.bfloat16: A.BF16, torch.float32: A.F32}
 _F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
 _SCORE = {"softmax": A.GATE_SOFTMAX, "sigmoid": A.GATE_SIGMOID}
 _ROUTING_OUT = {A.ROUTE_DENSE_I16: torch.int16, A.ROUTE_DENSE_I32: torch.int32, A.ROUTE_SPARSE_BOOL: torch.uint8}
 _FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
@@ -176,6 +177,116 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
                                             _ptr(grad_bias), _ptr(scratch), nbytes, _stream()),
             "moe_layer_norm_backward")
     return out, grad_weight, grad_bias
+
+
+class RmsNorm(NamedTuple):
+    """What rms_norm gives; None where it was not asked for."""
+    out: Optional[torch.Tensor]      # normalised rows [T,H]
+    codes: Optional[torch.Tensor]    # the same as e4m3 codes [T,H] ...
+    scales: Optional[torch.Tensor]   # ... with fp32 scales [T,H/128]
+    total: Optional[torch.Tensor]    # x + residual [T,H]
+    rstd: torch.Tensor               # [T] fp32
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+             residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+             want_rows: bool = True, quantize: bool = False, out: Optional[torch.Tensor] = None,
+             codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+             total: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None) -> RmsNorm:
+    """RMS norm of x + residual, rows [T,H] of bf16 or fp32 each (weight [H]
+    likewise).  The normalised rows come as ``out`` (of ``out_dtype``, default
+    x's; not with ``want_rows=False``), with ``quantize`` also or only as e4m3
+    codes and scales, as a Dispatcher with fp8 payload takes them.  ``total``,
+    of the residual's type, may be the residual itself (or x, where the types
+    are the same); without a residual it is written only where it is given."""
+    _need(x.dim() == 2, "x must be [T,H]")
+    T, H = x.shape
+    _check_rows(x, "x", (T, H), _ROW_DT)
+    wdt = _check_norm_params(H, weight=weight)
+    _need(want_rows or quantize, "rms_norm without rows needs quantize")
+    if residual is not None:
+        _check_rows(residual, "residual", (T, H), _ROW_DT)
+        if total is None:
+            total = torch.empty_like(residual)
+        _check_rows(total, "total", (T, H), (residual.dtype,))
+    elif total is not None:
+        _check_rows(total, "total", (T, H), _ROW_DT)
+    if want_rows:
+        if out is None:
+            out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=x.device)
+        _check_rows(out, "out", (T, H), _ROW_DT)
+        _need(out_dtype is None or out.dtype == out_dtype, "out must be of out_dtype")
+    else:
+        _need(out is None and out_dtype is None, "out and out_dtype need want_rows")
+    if quantize:
+        if H % 128:
+            raise ValueError(f"8-bit rows need a width that is a multiple of 128, got {H}")
+        if codes is None:
+            codes = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
+        if scales is None:
+            scales = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
+        _check_rows(codes, "codes", (T, H), _FP8_DTYPES)
+        _check_rows(scales, "scales", (T, H // 128), _F32)
+    else:
+        _need(codes is None and scales is None, "codes and scales need quantize")
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check_rows(rstd, "rstd", (T,), _F32)
+    _check_current_device((("x", x), ("weight", weight), ("residual", residual), ("out", out), ("codes", codes),
+                           ("scales", scales), ("total", total), ("rstd", rstd)))
+    A.check(A.lib().moe_rms_norm(T, H, _ROW_DT[x.dtype], _ROW_DT[(x if total is None else total).dtype],
+                                 A.BF16 if out is None else _ROW_DT[out.dtype], wdt, _ptr(x), _ptr(residual),
+                                 _ptr(weight), float(eps), _ptr(out), _ptr(codes), _ptr(scales), _ptr(total),
+                                 _ptr(rstd), _stream()), "moe_rms_norm")
+    return RmsNorm(out, codes, scales, total, rstd)
+
+
+def rms_norm_backward_scratch_bytes(T: int, H: int) -> int:
+    return int(A.lib().moe_rms_norm_backward_scratch_bytes(int(T), int(H)))
+
+
+def rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor,
+                      weight: Optional[torch.Tensor] = None, *, grad_total: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                      scratch: Optional[torch.Tensor] = None, want_weight: bool = True):
+    """Gradients of an RMS norm: (grad [T,H] of total's dtype, grad_weight [H]
+    fp32 or None without ``want_weight``).  ``total`` and ``rstd`` are the
+    forward's (x where there was no residual).  ``grad`` is the gradient of x
+    and of the residual alike; ``grad_total``, of total's dtype, is what
+    reaches the sum along the residual stream and may be ``out``."""
+    _need(total.dim() == 2, "total must be [T,H]")
+    T, H = total.shape
+    _check_rows(total, "total", (T, H), _ROW_DT)
+    _check_rows(grad_y, "grad_y", (T, H), _ROW_DT)
+    _check_rows(rstd, "rstd", (T,), _F32)
+    wdt = _check_norm_params(H, weight=weight)
+    if grad_total is not None:
+        _check_rows(grad_total, "grad_total", (T, H), (total.dtype,))
+    if out is None:
+        out = torch.empty_like(total)
+    _check_rows(out, "out", (T, H), (total.dtype,))
+    if want_weight:
+        if grad_weight is None:
+            grad_weight = torch.empty(H, dtype=torch.float32, device=total.device)
+        _check_rows(grad_weight, "grad_weight", (H,), _F32)
+        need = rms_norm_backward_scratch_bytes(T, H)
+        if need == 0:
+            raise ValueError(f"rows of {H} elements are outside 1..{A.NORM_MAX_H}")
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=total.device)
+        _need(scratch.is_contiguous(), "scratch must be contiguous")
+        if _nbytes(scratch) < need:
+            raise ValueError(f"scratch holds fewer than the {need} bytes needed")
+    else:
+        _need(grad_weight is None, "grad_weight needs want_weight")
+    _check_current_device((("grad_y", grad_y), ("total", total), ("rstd", rstd), ("weight", weight),
+                           ("grad_total", grad_total), ("out", out), ("grad_weight", grad_weight),
+                           ("scratch", scratch)))
+    A.check(A.lib().moe_rms_norm_backward(T, H, _ROW_DT[total.dtype], _ROW_DT[grad_y.dtype], wdt, _ptr(grad_y),
+                                          _ptr(total), _ptr(rstd), _ptr(weight), _ptr(grad_total), _ptr(out),
+                                          _ptr(grad_weight), _ptr(scratch), 0 if scratch is None else _nbytes(scratch),
+                                          _stream()), "moe_rms_norm_backward")
+    return out, grad_weight
 
 
 class Dispatcher:
@@ -681,6 +792,145 @@ class Dispatcher:
                                              _ptr(out), _ptr(grad_probs), _stream()), "moe_combine_backward")
         return out, grad_probs
 
+    # ---- expert products of a training step --------------------------------------
+    def _check_expert_weight(self, w, name, shape=None):
+        if w.dtype != torch.bfloat16 or w.dim() != 3 or w.shape[0] != self.E or (shape and w.shape != shape):
+            want = list(shape) if shape else f"[{self.E}, N, M]"
+            raise ValueError(f"{name} must be bf16 {want}, got {w.dtype} {list(w.shape)}")
+        if not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def grouped_product(self, rows: torch.Tensor, w: torch.Tensor, *, transpose: bool = False,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The product of every kept row with its expert's weight w [E,N,M]
+        (bf16, N and M multiples of 8): rows [R,M] -> out [R,N], or with
+        ``transpose`` rows [R,N] -> out [R,M], the gradient of the former to
+        its rows.  Rows of ``out`` that hold no kept copy are left as they
+        were."""
+        self._check_expert_weight(w, "w")
+        N, M = w.shape[1:]
+        cols, width = (N, M) if transpose else (M, N)
+        _check_rows(rows, "rows", (self.R, cols), _BF16)
+        if out is None:
+            out = torch.empty((self.R, width), dtype=torch.bfloat16, device=self.device)
+        _check_rows(out, "out", (self.R, width), _BF16)
+        _check_current_device((("the Dispatcher's workspace", self.ws), ("rows", rows), ("w", w), ("out", out)))
+        A.check(A.lib().moe_grouped_product(C.byref(self.h), N, M, 1 if transpose else 0, _ptr(rows), _ptr(w),
+                                            _ptr(out), _stream()), "moe_grouped_product")
+        return out
+
+    def grouped_weight_grad(self, grad: torch.Tensor, rows: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                            out_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False) -> torch.Tensor:
+        """The gradient of grouped_product to its weights: out [E,N,M] (bf16 or
+        fp32) = sum over an expert's kept rows of grad [R,N] times rows [R,M],
+        zeros for an expert without rows; with ``accumulate`` added to
+        ``out``."""
+        _need(grad.dim() == 2 and rows.dim() == 2, "grad and rows must be [R,N] and [R,M]")
+        N, M = grad.shape[1], rows.shape[1]
+        _check_rows(grad, "grad", (self.R, N), _BF16)
+        _check_rows(rows, "rows", (self.R, M), _BF16)
+        _need(out is not None or not accumulate, "accumulate needs out")
+        if out is None:
+            out = torch.empty((self.E, N, M), dtype=out_dtype, device=self.device)
+        _check_rows(out, "out", (self.E, N, M), _ROW_DT)
+        _check_current_device((("the Dispatcher's workspace", self.ws), ("grad", grad), ("rows", rows), ("out", out)))
+        A.check(A.lib().moe_grouped_weight_grad(C.byref(self.h), N, M, _ROW_DT[out.dtype], 1 if accumulate else 0,
+                                                _ptr(grad), _ptr(rows), _ptr(out), _stream()),
+                "moe_grouped_weight_grad")
+        return out
+
+    def grouped_mlp_keep(self, perm: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, *,
+                         h: Optional[torch.Tensor] = None, scratch: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None):
+        """grouped_mlp with bf16 weights (H and F multiples of 8) for a training
+        step: (out [R,H], h [R,2F]), with h, FC1's pre-activations, for
+        grouped_mlp_backward.  ``scratch`` is grouped_mlp's."""
+        F = self._check_mlp_pair(w1, w2)
+        _check_rows(perm, "perm", (self.R, self.H), _BF16)
+        if h is None:
+            h = torch.empty((self.R, 2 * F), dtype=torch.bfloat16, device=self.device)
+        if out is None:
+            out = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
+        if scratch is None:
+            scratch = self.alloc_mlp_scratch(F)
+        _check_rows(h, "h", (self.R, 2 * F), _BF16)
+        _check_rows(out, "out", (self.R, self.H), _BF16)
+        self._check_scratch(scratch, F, "bf16")
+        _check_current_device((("the Dispatcher's workspace", self.ws), ("perm", perm), ("w1", w1), ("w2", w2),
+                               ("h", h), ("out", out), ("scratch", scratch)))
+        A.check(A.lib().moe_grouped_mlp_keep(C.byref(self.h), F, _ptr(perm), _ptr(w1), _ptr(w2), _ptr(scratch),
+                                             _nbytes(scratch), _ptr(h), _ptr(out), _stream()), "moe_grouped_mlp_keep")
+        return out, h
+
+    def _check_mlp_pair(self, w1, w2) -> int:
+        self._check_expert_weight(w1, "w1")
+        F = w1.shape[1] // 2
+        self._check_expert_weight(w1, "w1", (self.E, 2 * F, self.H))
+        self._check_expert_weight(w2, "w2", (self.E, self.H, F))
+        return F
+
+    def mlp_backward_scratch_bytes(self, F: int) -> int:
+        return int(A.lib().moe_mlp_backward_scratch_bytes(C.byref(self.h), int(F)))
+
+    def alloc_mlp_backward_scratch(self, F: int) -> torch.Tensor:
+        n = self.mlp_backward_scratch_bytes(F)
+        _need(n > 0, "the FFN width must be a multiple of 8")
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def grouped_mlp_backward(self, grad_out: torch.Tensor, perm: torch.Tensor, h: torch.Tensor, w1: torch.Tensor,
+                             w2: torch.Tensor, *, grad_perm: Optional[torch.Tensor] = None,
+                             grad_w1: Optional[torch.Tensor] = None, grad_w2: Optional[torch.Tensor] = None,
+                             grad_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
+                             want_rows: bool = True, want_weights: bool = True,
+                             scratch: Optional[torch.Tensor] = None):
+        """Gradients of grouped_mlp_keep from that of its output (as
+        combine_backward gives it): (grad_perm [R,H], as dispatch_backward
+        takes it, grad_w1, grad_w2), the last two of ``grad_dtype`` (bf16 or
+        fp32) or of the type of the tensors given; with ``accumulate`` they are
+        added to those.  None without ``want_rows`` / ``want_weights``."""
+        F = self._check_mlp_pair(w1, w2)
+        _check_rows(grad_out, "grad_out", (self.R, self.H), _BF16)
+        _check_rows(perm, "perm", (self.R, self.H), _BF16)
+        _check_rows(h, "h", (self.R, 2 * F), _BF16)
+        if want_rows:
+            if grad_perm is None:
+                grad_perm = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
+            _check_rows(grad_perm, "grad_perm", (self.R, self.H), _BF16)
+        else:
+            _need(grad_perm is None, "grad_perm needs want_rows")
+        if want_weights:
+            _need(not accumulate or (grad_w1 is not None and grad_w2 is not None),
+                  "accumulate needs grad_w1 and grad_w2")
+            if grad_w1 is None:
+                grad_w1 = torch.empty(w1.shape, dtype=grad_dtype if grad_w2 is None else grad_w2.dtype,
+                                      device=self.device)
+            if grad_w2 is None:
+                grad_w2 = torch.empty(w2.shape, dtype=grad_w1.dtype, device=self.device)
+            _check_rows(grad_w1, "grad_w1", w1.shape, _ROW_DT)
+            _check_rows(grad_w2, "grad_w2", w2.shape, (grad_w1.dtype,))
+        else:
+            _need(grad_w1 is None and grad_w2 is None and not accumulate,
+                  "grad_w1, grad_w2 and accumulate need want_weights")
+        if scratch is None:
+            scratch = self.alloc_mlp_backward_scratch(F)
+        _need(scratch.is_contiguous(), "scratch must be contiguous")
+        need = self._scratch_need.get((F, "backward"))
+        if need is None:
+            need = self._scratch_need[F, "backward"] = self.mlp_backward_scratch_bytes(F)
+        if need <= 0:
+            raise ValueError(f"invalid FFN width {F}")
+        if _nbytes(scratch) < need:
+            raise ValueError(f"scratch holds fewer than the {need} bytes needed")
+        _check_current_device((("the Dispatcher's workspace", self.ws), ("grad_out", grad_out), ("perm", perm),
+                               ("h", h), ("w1", w1), ("w2", w2), ("grad_perm", grad_perm), ("grad_w1", grad_w1),
+                               ("grad_w2", grad_w2), ("scratch", scratch)))
+        A.check(A.lib().moe_grouped_mlp_backward(C.byref(self.h), F,
+                                                 A.BF16 if grad_w1 is None else _ROW_DT[grad_w1.dtype],
+                                                 1 if accumulate else 0, _ptr(grad_out), _ptr(perm), _ptr(h), _ptr(w1),
+                                                 _ptr(w2), _ptr(scratch), _nbytes(scratch), _ptr(grad_perm),
+                                                 _ptr(grad_w1), _ptr(grad_w2), _stream()), "moe_grouped_mlp_backward")
+        return grad_perm, grad_w1, grad_w2
+
     def decode_layer_scratch_bytes(self, F: int) -> int:
         return int(A.lib().moe_decode_layer_scratch_bytes(C.byref(self.h), int(F)))
 
@@ -745,10 +995,14 @@ class Dispatcher:
 
     def layer(self, x, routing, probs, w1, w2, *, perm=None, perm_scales=None, scratch=None, expert_out=None,
               out=None, w1_scales=None, w2_scales=None, T_live=None, apply_probs=True, check_overflow=False,
-              norm=None, router=None, gate=None):
+              norm=None, router=None, gate=None, rms=None, residual=None):
         """dispatch -> grouped MLP -> combine on the current stream.  With
         ``norm`` = (weight, bias) or (weight, bias, eps), the layer reads
-        layer_norm(x) in bf16 in place of x.  With ``router``, a callable that takes the
+        layer_norm(x) in bf16 in place of x.  With ``rms`` = (weight,) or
+        (weight, eps), it reads rms_norm(x + residual), and ``residual`` (if
+        given) becomes x + residual; with a handle of fp8 payload the norm
+        writes the codes that the dispatch takes, and bf16 rows for the
+        router alone.  With ``router``, a callable that takes the
         rows the layer reads and returns their logits [T,E], routing and probs
         (None then) are ``self.gate`` of those logits, with the keyword
         arguments ``gate`` (bias, score, normalize, scale).  With a
@@ -759,17 +1013,26 @@ class Dispatcher:
         (no host wait; capturable).  Buffers the caller omits are allocated
         per call."""
         _need(router is not None or gate is None, "gate needs a router")
+        _need(norm is None or rms is None, "norm and rms exclude each other")
+        _need(rms is not None or residual is None, "residual needs rms")
+        _need(router is None or (routing is None and probs is None), "routing and probs come from the router's logits")
+        x_scales = None
         if norm is not None:
             x, _, _ = layer_norm(x, *norm, out_dtype=torch.bfloat16)
+        elif rms is not None:
+            fp8 = self.payload == A.FP8E4M3_B128
+            rows = router is not None or not fp8
+            normed = rms_norm(x, *rms, residual=residual, total=residual, want_rows=rows, quantize=fp8,
+                              out_dtype=torch.bfloat16 if rows else None)
+            x, x_scales = (normed.codes, normed.scales) if fp8 else (normed.out, None)
         if router is not None:
-            _need(routing is None and probs is None, "routing and probs come from the router's logits")
-            routing, probs = self.gate(router(x), **(gate or {}))
+            routing, probs = self.gate(router(x if x_scales is None else normed.out), **(gate or {}))
         if self.payload == A.FP8E4M3_B128 and x.dtype == torch.bfloat16:
             _, flag = self.preprocess(routing, probs, T_live)
             perm, perm_scales = self.permute_quantize(x, out=perm, out_scales=perm_scales)
         else:
-            perm, _, flag, _, perm_scales = self.dispatch(x, routing, probs, out=perm, out_scales=perm_scales,
-                                                          T_live=T_live)
+            perm, _, flag, _, perm_scales = self.dispatch(x, routing, probs, x_scales=x_scales, out=perm,
+                                                          out_scales=perm_scales, T_live=T_live)
         y = self.grouped_mlp(perm, w1, w2, w1_scales=w1_scales, w2_scales=w2_scales, scratch=scratch,
                              out=expert_out, perm_scales=perm_scales)
         y = self.combine(y, apply_probs=apply_probs, out=out)

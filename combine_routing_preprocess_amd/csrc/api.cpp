@@ -8,6 +8,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <unordered_map>
 
@@ -606,6 +607,184 @@ int moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dty
     if (overlap(d_grad_x, nx, d_x, nx) || overlap(d_grad_x, nx, d_grad_y, row_bytes(T, H, y_dtype))) return MOE_EINVAL;
     return hip_rc(launch_layer_norm_backward(T, H, x_dtype, y_dtype, w_dtype, d_grad_y, d_x, d_mean, d_rstd, d_weight,
                                              d_grad_x, d_grad_weight, d_grad_bias, d_scratch, (hipStream_t)stream));
+}
+
+namespace {
+
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+// An output may overlap none of the others (empty and null ones overlap nothing).
+bool overlaps_any(Span out, std::initializer_list<Span> others) {
+    for (const Span& o : others)
+        if (out.p && o.p && out.n && o.n && overlap(out.p, out.n, o.p, o.n)) return true;
+    return false;
+}
+
+bool grouped_size(int64_t v) { return v >= 8 && v <= MOE_GROUPED_MAX && v % 8 == 0; }
+
+int check_grouped(const moe_handle* h, int64_t N, int64_t M) {
+    int rc = check_handle(h, true);
+    if (rc) return rc;
+    return grouped_size(N) && grouped_size(M) && N * M <= (1ll << 30) ? MOE_OK : MOE_ESHAPE;
+}
+
+// Bytes of R rows and of E weights.
+size_t rows_span(const moe_handle* h, int64_t width) { return (size_t)h->desc.out_rows * width * 2; }
+size_t weight_span(const moe_handle* h, int64_t N, int64_t M, int32_t dtype) {
+    return (size_t)h->desc.E * N * M * (dtype == MOE_BF16 ? 2 : 4);
+}
+
+}  // namespace
+
+int moe_grouped_product(const moe_handle* h, int32_t N, int32_t M, int32_t transpose, const void* d_rows,
+                        const void* d_w, void* d_out, void* stream) {
+    int rc = check_grouped(h, N, M);
+    if (rc) return rc;
+    if (!d_w || (h->desc.out_rows > 0 && (!d_rows || !d_out))) return MOE_EINVAL;
+    if (!al16(d_rows) || !al16(d_w) || !al16(d_out)) return MOE_EALIGN;
+    if (overlaps_any({d_out, rows_span(h, transpose ? M : N)},
+                     {{d_rows, rows_span(h, transpose ? N : M)}, {d_w, weight_span(h, N, M, MOE_BF16)}}))
+        return MOE_EINVAL;
+    return hip_rc(launch_grouped_product(h, N, M, transpose ? 1 : 0, d_rows, d_w, d_out, (hipStream_t)stream));
+}
+
+int moe_grouped_weight_grad(const moe_handle* h, int32_t N, int32_t M, int32_t out_dtype, int32_t accumulate,
+                            const void* d_grad, const void* d_rows, void* d_out, void* stream) {
+    int rc = check_grouped(h, N, M);
+    if (rc) return rc;
+    if (!row_dtype(out_dtype)) return MOE_EDTYPE;
+    if (!d_out || (h->desc.out_rows > 0 && (!d_grad || !d_rows))) return MOE_EINVAL;
+    if (!al16(d_grad) || !al16(d_rows) || !al16(d_out)) return MOE_EALIGN;
+    if (overlaps_any({d_out, weight_span(h, N, M, out_dtype)},
+                     {{d_grad, rows_span(h, N)}, {d_rows, rows_span(h, M)}}))
+        return MOE_EINVAL;
+    return hip_rc(launch_grouped_weight_grad(h, N, M, out_dtype, accumulate ? 1 : 0, d_grad, d_rows, d_out,
+                                             (hipStream_t)stream));
+}
+
+int moe_grouped_mlp_keep(const moe_handle* h, int32_t F, const void* d_perm, const void* d_w1, const void* d_w2,
+                         void* d_scratch, size_t scratch_bytes, void* d_h, void* d_expert_out, void* stream) {
+    if (!h) return MOE_EINVAL;
+    const int64_t H = h->desc.H;
+    int rc = check_grouped(h, 2 * (int64_t)F, H);
+    if (rc) return rc;
+    if (!grouped_size(F)) return MOE_ESHAPE;
+    if (!d_w1 || !d_w2 || !d_scratch || (h->desc.out_rows > 0 && (!d_perm || !d_h || !d_expert_out))) return MOE_EINVAL;
+    if (!al16(d_perm) || !al16(d_w1) || !al16(d_w2) || !al16(d_scratch) || !al16(d_h) || !al16(d_expert_out))
+        return MOE_EALIGN;
+    if (scratch_bytes < moe_mlp_scratch_bytes(h, F, MOE_BF16)) return MOE_ENOSPC;
+    const Span perm = {d_perm, rows_span(h, H)}, w1 = {d_w1, weight_span(h, 2 * F, H, MOE_BF16)},
+               w2 = {d_w2, weight_span(h, H, F, MOE_BF16)}, act = {d_scratch, rows_span(h, F)},
+               hh = {d_h, rows_span(h, 2 * F)}, out = {d_expert_out, rows_span(h, H)};
+    if (overlaps_any(act, {perm, w1, w2, hh, out}) || overlaps_any(hh, {perm, w1, w2, out}) ||
+        overlaps_any(out, {perm, w1, w2}))
+        return MOE_EINVAL;
+    rc = hip_rc(launch_grouped_swiglu_keep(h, F, d_perm, d_w1, d_h, d_scratch, (hipStream_t)stream));
+    if (rc) return rc;
+    return hip_rc(launch_grouped_product(h, (int)H, F, 0, d_scratch, d_w2, d_expert_out, (hipStream_t)stream));
+}
+
+size_t moe_mlp_backward_scratch_bytes(const moe_handle* h, int32_t F) {
+    if (!h || !grouped_size(F) || !grouped_size(2 * (int64_t)F)) return 0;
+    return up(rows_span(h, 2 * F), kAlign) + up(rows_span(h, F) + 1, kAlign);
+}
+
+int moe_grouped_mlp_backward(const moe_handle* h, int32_t F, int32_t w_dtype, int32_t accumulate,
+                             const void* d_grad_out, const void* d_perm, const void* d_h, const void* d_w1,
+                             const void* d_w2, void* d_scratch, size_t scratch_bytes, void* d_grad_perm,
+                             void* d_grad_w1, void* d_grad_w2, void* stream) {
+    if (!h) return MOE_EINVAL;
+    const int64_t H = h->desc.H;
+    int rc = check_grouped(h, 2 * (int64_t)F, H);
+    if (rc) return rc;
+    if (!grouped_size(F)) return MOE_ESHAPE;
+    if (!row_dtype(w_dtype)) return MOE_EDTYPE;
+    if (!d_w1 || !d_w2 || !d_scratch || (h->desc.out_rows > 0 && (!d_grad_out || !d_perm || !d_h))) return MOE_EINVAL;
+    if (!al16(d_grad_out) || !al16(d_perm) || !al16(d_h) || !al16(d_w1) || !al16(d_w2) || !al16(d_scratch) ||
+        !al16(d_grad_perm) || !al16(d_grad_w1) || !al16(d_grad_w2))
+        return MOE_EALIGN;
+    const size_t need = moe_mlp_backward_scratch_bytes(h, F);
+    if (scratch_bytes < need) return MOE_ENOSPC;
+    const Span gy = {d_grad_out, rows_span(h, H)}, x = {d_perm, rows_span(h, H)}, hh = {d_h, rows_span(h, 2 * F)},
+               w1 = {d_w1, weight_span(h, 2 * F, H, MOE_BF16)}, w2 = {d_w2, weight_span(h, H, F, MOE_BF16)},
+               tmp = {d_scratch, need}, gx = {d_grad_perm, rows_span(h, H)},
+               g1 = {d_grad_w1, weight_span(h, 2 * F, H, w_dtype)}, g2 = {d_grad_w2, weight_span(h, H, F, w_dtype)};
+    if (overlaps_any(tmp, {gy, x, hh, w1, w2, gx, g1, g2}) || overlaps_any(gx, {gy, x, hh, w1, w2, g1, g2}) ||
+        overlaps_any(g1, {gy, x, hh, w1, w2, g2}) || overlaps_any(g2, {gy, x, hh, w1, w2}))
+        return MOE_EINVAL;
+    hipStream_t s = (hipStream_t)stream;
+    void* gh = d_scratch;
+    void* act = (char*)d_scratch + up(rows_span(h, 2 * F), kAlign);
+    rc = hip_rc(launch_grouped_swiglu_grad(h, F, d_grad_out, d_w2, d_h, gh, act, s));
+    if (!rc && d_grad_w2)
+        rc = hip_rc(launch_grouped_weight_grad(h, (int)H, F, w_dtype, accumulate ? 1 : 0, d_grad_out, act, d_grad_w2, s));
+    if (!rc && d_grad_perm) rc = hip_rc(launch_grouped_product(h, 2 * F, (int)H, 1, gh, d_w1, d_grad_perm, s));
+    if (!rc && d_grad_w1)
+        rc = hip_rc(launch_grouped_weight_grad(h, 2 * F, (int)H, w_dtype, accumulate ? 1 : 0, gh, d_perm, d_grad_w1, s));
+    return rc;
+}
+
+int moe_rms_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t r_dtype, int32_t y_dtype, int32_t w_dtype,
+                 const void* d_x, const void* d_residual, const void* d_weight, float eps, void* d_y, void* d_codes,
+                 float* d_scales, void* d_total, float* d_rstd, void* stream) {
+    int rc = check_norm(T, H, x_dtype, y_dtype, w_dtype);
+    if (rc) return rc;
+    if (!row_dtype(r_dtype)) return MOE_EDTYPE;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return MOE_EINVAL;
+    if (d_codes || d_scales) {
+        if (H % 128) return MOE_ESHAPE;
+        if (T > 0 && (!d_codes || !d_scales)) return MOE_EINVAL;
+    }
+    if (T > 0 && (!d_x || (!d_y && !d_codes))) return MOE_EINVAL;
+    if (!al16(d_x) || !al16(d_residual) || !al16(d_weight) || !al16(d_y) || !al16(d_codes) || !al4(d_scales) ||
+        !al16(d_total) || !al4(d_rstd))
+        return MOE_EALIGN;
+    const Span x = {d_x, row_bytes(T, H, x_dtype)}, r = {d_residual, row_bytes(T, H, r_dtype)},
+               w = {d_weight, row_bytes(1, H, w_dtype)}, y = {d_y, row_bytes(T, H, y_dtype)},
+               q = {d_codes, (size_t)T * H}, sc = {d_scales, (size_t)T * (H / 128) * 4},
+               t = {d_total, row_bytes(T, H, r_dtype)}, rs = {d_rstd, (size_t)T * 4};
+    const Span none = {nullptr, 0};
+    const bool over_x = d_total == d_x && x_dtype == r_dtype, over_r = d_total == d_residual;
+    if (overlaps_any(y, {x, r, w, q, sc, t, rs}) || overlaps_any(q, {x, r, w, sc, t, rs}) ||
+        overlaps_any(sc, {x, r, w, t, rs}) || overlaps_any(rs, {x, r, w, t}) ||
+        overlaps_any(t, {over_x ? none : x, over_r ? none : r, w}))
+        return MOE_EINVAL;
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
+    return hip_rc(launch_rms_norm(T, H, x_dtype, r_dtype, y_dtype, w_dtype, d_x, d_residual, d_weight, eps, d_y,
+                                  d_codes, d_scales, d_total, d_rstd, ncu, (hipStream_t)stream));
+}
+
+size_t moe_rms_norm_backward_scratch_bytes(int32_t T, int32_t H) {
+    if (check_norm(T, H, MOE_F32, MOE_F32, MOE_F32)) return 0;
+    return up(rms_norm_backward_scratch_bytes(T, H) + 1, kAlign);
+}
+
+int moe_rms_norm_backward(int32_t T, int32_t H, int32_t t_dtype, int32_t y_dtype, int32_t w_dtype,
+                          const void* d_grad_y, const void* d_total, const float* d_rstd, const void* d_weight,
+                          const void* d_grad_total, void* d_grad, float* d_grad_weight, void* d_scratch,
+                          size_t scratch_bytes, void* stream) {
+    int rc = check_norm(T, H, t_dtype, y_dtype, w_dtype);
+    if (rc) return rc;
+    if (T > 0 && (!d_grad_y || !d_total || !d_rstd || !d_grad)) return MOE_EINVAL;
+    if (d_grad_weight && !d_scratch) return MOE_EINVAL;
+    if (!al16(d_grad_y) || !al16(d_total) || !al4(d_rstd) || !al16(d_weight) || !al16(d_grad_total) || !al16(d_grad) ||
+        !al16(d_grad_weight) || !al16(d_scratch))
+        return MOE_EALIGN;
+    if (d_grad_weight && scratch_bytes < moe_rms_norm_backward_scratch_bytes(T, H)) return MOE_ENOSPC;
+    const Span gy = {d_grad_y, row_bytes(T, H, y_dtype)}, t = {d_total, row_bytes(T, H, t_dtype)},
+               gt = {d_grad_total, row_bytes(T, H, t_dtype)}, g = {d_grad, row_bytes(T, H, t_dtype)},
+               w = {d_weight, row_bytes(1, H, w_dtype)}, rs = {d_rstd, (size_t)T * 4},
+               gw = {d_grad_weight, (size_t)H * 4}, tmp = {d_grad_weight ? d_scratch : nullptr, scratch_bytes};
+    const Span none = {nullptr, 0};
+    if (overlaps_any(g, {gy, t, d_grad == d_grad_total ? none : gt, w, rs, gw, tmp}) ||
+        overlaps_any(gw, {gy, t, gt, w, rs, tmp}) || overlaps_any(tmp, {gy, t, gt, w, rs}))
+        return MOE_EINVAL;
+    return hip_rc(launch_rms_norm_backward(T, H, t_dtype, y_dtype, w_dtype, d_grad_y, d_total, d_rstd, d_weight,
+                                           d_grad_total, d_grad, d_grad_weight, d_scratch, (hipStream_t)stream));
 }
 
 }  // extern "C"

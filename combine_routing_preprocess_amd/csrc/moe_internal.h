@@ -118,6 +118,24 @@ hipError_t launch_gate(const moe_handle* h, const void* logits, int logit_dtype,
 hipError_t launch_gate_backward(const moe_handle* h, const float* grad_probs, const void* logits, int logit_dtype,
                                 const void* routing, int sigmoid, int normalize, float scale, void* grad_logits,
                                 hipStream_t s);
+// products grouped by expert of bf16 rows [R, ..] with weights [E,N,M], the
+// weights' gradients, and the products around SwiGLU in training
+hipError_t launch_grouped_product(const moe_handle* h, int N, int M, int transpose, const void* rows, const void* w,
+                                  void* out, hipStream_t s);
+hipError_t launch_grouped_weight_grad(const moe_handle* h, int N, int M, int out_dtype, int accumulate,
+                                      const void* grad, const void* rows, void* out, hipStream_t s);
+hipError_t launch_grouped_swiglu_keep(const moe_handle* h, int F, const void* rows, const void* w1, void* hout,
+                                      void* act, hipStream_t s);
+hipError_t launch_grouped_swiglu_grad(const moe_handle* h, int F, const void* grad_out, const void* w2,
+                                      const void* hin, void* grad_h, void* act, hipStream_t s);
+// RMS norm of rows and its backward pass
+size_t rms_norm_backward_scratch_bytes(int T, int H);
+hipError_t launch_rms_norm(int T, int H, int x_dtype, int r_dtype, int y_dtype, int w_dtype, const void* x,
+                           const void* residual, const void* weight, float eps, void* y, void* codes, float* scales,
+                           void* total, float* rstd, int num_cu, hipStream_t s);
+hipError_t launch_rms_norm_backward(int T, int H, int t_dtype, int y_dtype, int w_dtype, const void* gy,
+                                    const void* total, const float* rstd, const void* weight, const void* grad_total,
+                                    void* gx, float* gw, void* scratch, hipStream_t s);
 // persistent decode layer (quantise-on-dispatch, FC1, activation quantiser,
 // FC2, combine in one launch after a control-block reset)
 size_t decode_layer_scratch_bytes(long long R, int H, int F);

@@ -526,6 +526,114 @@ int moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dty
                             const void* d_weight, void* d_grad_x, float* d_grad_weight, float* d_grad_bias,
                             void* d_scratch, size_t scratch_bytes, void* stream);
 
+/* ---- expert products of a training step --------------------------------------
+ * Matrix products grouped by expert over the dispatched rows, for any sizes
+ * that are multiples of 8, and the two passes of the SwiGLU MLP that a training
+ * step makes of them.  [P1] "Configuration" (grouped FC1 -> activation -> FC2
+ * over dispatched rows), [P2] "Full HybridEP reference validation" (gradients
+ * of the hidden states).  "Rows of e" are the kept rows of expert e's segment
+ * (moe_handle); all sums are fp32 of exact bf16 products, rounded once to the
+ * output's type.  Rows that hold no kept copy are neither read nor written.
+ * Rows are bf16 whatever the handle's payload; the handle needs routing
+ * metadata.  Common requirements: N, M, H, F multiples of 8, from 8 to
+ * MOE_GROUPED_MAX, N * M <= 2^30 (MOE_ESHAPE); arrays 16-byte aligned; outputs
+ * overlap neither inputs nor each other (MOE_EINVAL). */
+#define MOE_GROUPED_MAX 65536
+
+/* out_r = w_e rows_r, or with `transpose` out_r = w_e^T rows_r (the gradient of
+ * the former to its rows), for every row r of every expert e.
+ *   d_w     [E,N,M] bf16
+ *   d_rows  [R,M] bf16 ([R,N] with transpose)
+ *   d_out   [R,N] bf16 out ([R,M] with transpose) */
+int moe_grouped_product(const moe_handle* h, int32_t N, int32_t M, int32_t transpose, const void* d_rows,
+                        const void* d_w, void* d_out, void* stream);
+
+/* The gradient of moe_grouped_product to its weights: out_e[n][m] = sum over
+ * the rows r of e of grad_r[n] * rows_r[m], in a fixed order (a call repeats
+ * bit for bit).  Written fresh, zeros for experts without rows, or with
+ * `accumulate` added to what d_out holds.
+ *   out_dtype  MOE_BF16 or MOE_F32 (else MOE_EDTYPE)
+ *   d_grad     [R,N] bf16
+ *   d_rows     [R,M] bf16
+ *   d_out      [E,N,M] of out_dtype */
+int moe_grouped_weight_grad(const moe_handle* h, int32_t N, int32_t M, int32_t out_dtype, int32_t accumulate,
+                            const void* d_grad, const void* d_rows, void* d_out, void* stream);
+
+/* moe_grouped_swiglu_mlp with bf16 weights, keeping FC1's sums for the backward
+ * pass: h = W1 x, a = silu(h[0:F]) * h[F:2F] from the unrounded sums, y = W2 a
+ * of a in bf16.
+ *   d_perm        [R,H] bf16
+ *   d_w1, d_w2    [E,2F,H], [E,H,F] bf16
+ *   d_scratch     >= moe_mlp_scratch_bytes(h, F, MOE_BF16) bytes
+ *   d_h           [R,2F] bf16 out
+ *   d_expert_out  [R,H] bf16 out */
+int moe_grouped_mlp_keep(const moe_handle* h, int32_t F, const void* d_perm, const void* d_w1, const void* d_w2,
+                         void* d_scratch, size_t scratch_bytes, void* d_h, void* d_expert_out, void* stream);
+
+/* Its backward pass, from the kept h = (g, u) and the gradient of the expert
+ * output (moe_combine_backward): with s = sigmoid(g) and da = W2^T grad_out,
+ *   grad_h = (da u s (1 + g (1 - s)), da g s), a = g s u, both rounded to bf16,
+ *   grad_perm = W1^T grad_h,  grad_w1 = sum grad_h x^T,  grad_w2 = sum grad_out a^T.
+ * grad_perm is what moe_dispatch_backward takes.  A null gradient is not
+ * computed.
+ *   w_dtype, accumulate  of the weight gradients, as moe_grouped_weight_grad
+ *   d_grad_out  [R,H] bf16
+ *   d_perm      [R,H] bf16, the forward's rows; read for d_grad_w1
+ *   d_h         [R,2F] bf16
+ *   d_scratch   >= moe_mlp_backward_scratch_bytes(h, F) bytes (MOE_ENOSPC): grad_h
+ *               and a; two calls that share it must not overlap
+ *   d_grad_perm nullable [R,H] bf16 out
+ *   d_grad_w1, d_grad_w2  nullable [E,2F,H], [E,H,F] of w_dtype */
+size_t moe_mlp_backward_scratch_bytes(const moe_handle* h, int32_t F);
+int moe_grouped_mlp_backward(const moe_handle* h, int32_t F, int32_t w_dtype, int32_t accumulate,
+                             const void* d_grad_out, const void* d_perm, const void* d_h, const void* d_w1,
+                             const void* d_w2, void* d_scratch, size_t scratch_bytes, void* d_grad_perm,
+                             void* d_grad_w1, void* d_grad_w2, void* stream);
+
+/* ---- RMS norm with the residual's addition (rows in front of the layer) ------
+ * t = x + residual, r = 1 / sqrt(mean(t^2) + eps), y = t * r * weight per row,
+ * in fp32 from the unrounded t.  The rows come out as bf16 or fp32 (d_y), as
+ * e4m3 codes with one fp32 scale per 128 columns (d_codes, d_scales: what
+ * moe_dispatch takes with fp8 payload; scale = block max / 448, 1 for an
+ * all-zero block, code = e4m3(y / scale), nearest-even), or both at once.  A
+ * block with a NaN or an infinity has the scale NaN.  No handle; limits and
+ * alignment as moe_layer_norm, with H a multiple of 128 for codes (MOE_ESHAPE).
+ *   x_dtype, r_dtype, y_dtype, w_dtype  MOE_BF16 or MOE_F32 each (MOE_EDTYPE):
+ *                  of d_x, of d_residual and d_total, of d_y, of d_weight
+ *   d_residual     nullable [T,H]
+ *   d_weight       nullable [H] (1 where absent)
+ *   d_y            nullable [T,H] out; d_codes, d_scales nullable out [T,H] e4m3
+ *                  and [T,H/128] fp32, both or neither; not all three null
+ *   d_total        nullable [T,H] out of r_dtype: t, the new residual stream and
+ *                  what the backward pass reads; may be d_residual, or d_x where
+ *                  the types are the same; no other overlap (MOE_EINVAL)
+ *   d_rstd         nullable [T] fp32 out: r */
+int moe_rms_norm(int32_t T, int32_t H, int32_t x_dtype, int32_t r_dtype, int32_t y_dtype, int32_t w_dtype,
+                 const void* d_x, const void* d_residual, const void* d_weight, float eps, void* d_y, void* d_codes,
+                 float* d_scales, void* d_total, float* d_rstd, void* stream);
+
+/* Backward of the RMS norm.  With xh = t * r and q = grad_y * weight:
+ * grad = grad_total + r * (q - xh * mean(q * xh)) per row, the gradient of x and
+ * of the residual alike, and grad_weight = sum over the rows of grad_y * xh in
+ * fp32, in a fixed order (a call repeats bit for bit), written fresh (zeros
+ * when T = 0).
+ *   t_dtype       of d_total, d_grad_total and d_grad
+ *   d_grad_y      [T,H] of y_dtype
+ *   d_total, d_rstd  the forward's t (x without a residual) and r
+ *   d_weight      nullable [H] of w_dtype
+ *   d_grad_total  nullable [T,H]: the gradient that reaches t along the residual
+ *                 stream
+ *   d_grad        [T,H] out; may be d_grad_total, no other overlap (MOE_EINVAL)
+ *   d_grad_weight nullable [H] fp32 out
+ *   d_scratch     >= moe_rms_norm_backward_scratch_bytes(T, H) bytes
+ *                 (MOE_ENOSPC); two calls that share it must not overlap.  May
+ *                 be NULL without d_grad_weight. */
+size_t moe_rms_norm_backward_scratch_bytes(int32_t T, int32_t H);
+int moe_rms_norm_backward(int32_t T, int32_t H, int32_t t_dtype, int32_t y_dtype, int32_t w_dtype,
+                          const void* d_grad_y, const void* d_total, const float* d_rstd, const void* d_weight,
+                          const void* d_grad_total, void* d_grad, float* d_grad_weight, void* d_scratch,
+                          size_t scratch_bytes, void* stream);
+
 /* ---- caller-owned buffer ring ------------------------------------------------
  * [P1] "Summary", "Motivation", "Known limitations": dispatch outputs and FC2
  * outputs live in a fixed ring of persistent slots owned by the application;
