@@ -648,7 +648,9 @@ int moe_grouped_product(const moe_handle* h, int32_t N, int32_t M, int32_t trans
     if (overlaps_any({d_out, rows_span(h, transpose ? M : N)},
                      {{d_rows, rows_span(h, transpose ? N : M)}, {d_w, weight_span(h, N, M, MOE_BF16)}}))
         return MOE_EINVAL;
-    return hip_rc(launch_grouped_product(h, N, M, transpose ? 1 : 0, d_rows, d_w, d_out, (hipStream_t)stream));
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
+    return hip_rc(launch_grouped_product(h, N, M, transpose ? 1 : 0, d_rows, d_w, d_out, ncu, (hipStream_t)stream));
 }
 
 int moe_grouped_weight_grad(const moe_handle* h, int32_t N, int32_t M, int32_t out_dtype, int32_t accumulate,
@@ -661,7 +663,9 @@ int moe_grouped_weight_grad(const moe_handle* h, int32_t N, int32_t M, int32_t o
     if (overlaps_any({d_out, weight_span(h, N, M, out_dtype)},
                      {{d_grad, rows_span(h, N)}, {d_rows, rows_span(h, M)}}))
         return MOE_EINVAL;
-    return hip_rc(launch_grouped_weight_grad(h, N, M, out_dtype, accumulate ? 1 : 0, d_grad, d_rows, d_out,
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
+    return hip_rc(launch_grouped_weight_grad(h, N, M, out_dtype, accumulate ? 1 : 0, d_grad, d_rows, d_out, ncu,
                                              (hipStream_t)stream));
 }
 
@@ -682,9 +686,11 @@ int moe_grouped_mlp_keep(const moe_handle* h, int32_t F, const void* d_perm, con
     if (overlaps_any(act, {perm, w1, w2, hh, out}) || overlaps_any(hh, {perm, w1, w2, out}) ||
         overlaps_any(out, {perm, w1, w2}))
         return MOE_EINVAL;
-    rc = hip_rc(launch_grouped_swiglu_keep(h, F, d_perm, d_w1, d_h, d_scratch, (hipStream_t)stream));
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
+    rc = hip_rc(launch_grouped_swiglu_keep(h, F, d_perm, d_w1, d_h, d_scratch, ncu, (hipStream_t)stream));
     if (rc) return rc;
-    return hip_rc(launch_grouped_product(h, (int)H, F, 0, d_scratch, d_w2, d_expert_out, (hipStream_t)stream));
+    return hip_rc(launch_grouped_product(h, (int)H, F, 0, d_scratch, d_w2, d_expert_out, ncu, (hipStream_t)stream));
 }
 
 size_t moe_mlp_backward_scratch_bytes(const moe_handle* h, int32_t F) {
@@ -715,15 +721,19 @@ int moe_grouped_mlp_backward(const moe_handle* h, int32_t F, int32_t w_dtype, in
     if (overlaps_any(tmp, {gy, x, hh, w1, w2, gx, g1, g2}) || overlaps_any(gx, {gy, x, hh, w1, w2, g1, g2}) ||
         overlaps_any(g1, {gy, x, hh, w1, w2, g2}) || overlaps_any(g2, {gy, x, hh, w1, w2}))
         return MOE_EINVAL;
+    const int ncu = num_cu();
+    if (ncu <= 0) return MOE_EHIP;
     hipStream_t s = (hipStream_t)stream;
     void* gh = d_scratch;
     void* act = (char*)d_scratch + up(rows_span(h, 2 * F), kAlign);
-    rc = hip_rc(launch_grouped_swiglu_grad(h, F, d_grad_out, d_w2, d_h, gh, act, s));
+    rc = hip_rc(launch_grouped_swiglu_grad(h, F, d_grad_out, d_w2, d_h, gh, act, ncu, s));
     if (!rc && d_grad_w2)
-        rc = hip_rc(launch_grouped_weight_grad(h, (int)H, F, w_dtype, accumulate ? 1 : 0, d_grad_out, act, d_grad_w2, s));
-    if (!rc && d_grad_perm) rc = hip_rc(launch_grouped_product(h, 2 * F, (int)H, 1, gh, d_w1, d_grad_perm, s));
+        rc = hip_rc(launch_grouped_weight_grad(h, (int)H, F, w_dtype, accumulate ? 1 : 0, d_grad_out, act, d_grad_w2, ncu,
+                                               s));
+    if (!rc && d_grad_perm) rc = hip_rc(launch_grouped_product(h, 2 * F, (int)H, 1, gh, d_w1, d_grad_perm, ncu, s));
     if (!rc && d_grad_w1)
-        rc = hip_rc(launch_grouped_weight_grad(h, 2 * F, (int)H, w_dtype, accumulate ? 1 : 0, gh, d_perm, d_grad_w1, s));
+        rc = hip_rc(launch_grouped_weight_grad(h, 2 * F, (int)H, w_dtype, accumulate ? 1 : 0, gh, d_perm, d_grad_w1, ncu,
+                                               s));
     return rc;
 }
 

@@ -9,109 +9,20 @@
 //   its transpose      the same with w read across its rows (k = row of w)
 //   weight's gradient  a = column of the rows, b = column of the gradient, k = row (both read across)
 // An operand is "across" when its k runs over rows of the array.
-#include "moe_internal.h"
+#include "grouped.h"
 
 namespace moe {
+
+using namespace grouped;
+
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// What happens to the sums.
-enum Epilogue {
-    kRows,         // out[row][a] in bf16
-    kSwigluKeep,   // a = gate and up of a feature: h and silu(gate) * up, both in bf16
-    kSwigluGrad,   // the sums are the activation's gradient: h's gradient and the activation again
-    kWeight16,     // out[e][b][a] in bf16
-    kWeight16Add,  // the same, added to what is there
-    kWeight32      // the same in fp32, added to what is there or not
-};
-
-struct Args {
-    const uint16_t* a;     // [E] x [.., ..] weights, or rows (weight's gradient)
-    const uint16_t* b;     // rows
-    const uint16_t* h;     // kSwigluGrad: the forward's pre-activations [R, 2 na]
-    void* out;
-    uint16_t* out2;        // kSwigluKeep, kSwigluGrad: activations [R, na]
-    const int64_t* seg_off;
-    const int32_t* kept;
-    long long R;
-    int E, na, nb, nk;     // features, columns of the gradient (weight's gradient), sum's length
-    int accumulate;
-};
 
 constexpr int kTA = 256;                    // features of a tile: 64 per wavefront
 constexpr int kTB = 128;                    // rows (weight's gradient: columns of the gradient) of a tile
 constexpr int kBK = 32;                     // sum's elements per stage
 constexpr int kSlots = 3;                   // stages in LDS
 constexpr int kABytes = kTA * kBK * 2, kBBytes = kTB * kBK * 2, kSlot = kABytes + kBBytes;
-constexpr int kNxcd = 8;
 constexpr int kPerThread = kMaxE / 256;     // experts whose tiles one thread counts
-
-typedef __attribute__((address_space(1))) const char gchar;
-typedef __attribute__((address_space(3))) char lchar;
-typedef short i16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4 li16x4;
-typedef __attribute__((address_space(3))) u32x4 lu32x4;
-typedef __attribute__((address_space(3))) u32x2 lu32x2;
-
-__device__ __forceinline__ gchar* uniform_ptr(const void* p) {
-    const uint64_t v = (uint64_t)(uintptr_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (gchar*)(((uint64_t)hi << 32) | lo);
-}
-__device__ __forceinline__ int uniform(int v) { return (int)__builtin_amdgcn_readfirstlane((uint32_t)v); }
-
-// 16 bytes per lane from sbase (wave-uniform) + voff (per lane) to LDS byte
-// address lds + 16 * lane.  Inline asm, so that the compiler does not wait for
-// it before other LDS reads; completion is awaited explicitly.  m0 is written
-// only here; a load to LDS needs one wait state after that (s_nop 0).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void to_lds16(gchar* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// At most n of this wavefront's transfers in flight.
-__device__ __forceinline__ void wait_transfers(int n) {
-    if (n == 6) wait_vm<6>();
-    else if (n == 5) wait_vm<5>();
-    else if (n == 4) wait_vm<4>();
-    else wait_vm<0>();
-}
-// Workgroup barrier; this wavefront's LDS reads are complete before it
-// arrives, its transfers may be in flight.
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// Between a wavefront's LDS writes and its other lanes' reads of them: the
-// hardware keeps their order, the compiler has to be told.
-__device__ __forceinline__ void lanes_exchange() { asm volatile("" ::: "memory"); }
-
-__device__ __forceinline__ int expert_rows(const Args& p, int e, long long* seg) {
-    const long long so = p.seg_off[e];
-    long long m = so < p.R ? (long long)p.kept[e] : 0;
-    if (so + m > p.R) m = p.R - so;
-    *seg = so;
-    return (int)m;
-}
-
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
-
-// One tile: na, nb, nk bound the operands' columns, rows and sums; a0, b0 are
-// the tile's first feature and row (column of the gradient).
-struct Tile {
-    gchar* A;
-    gchar* B;
-    int a0, b0, nb, nk;
-};
 
 // A stage's transfers.  Not across: rows of 64 bytes, four chunks of 16, chunk
 // c of row r at place c ^ (r / 4) % 4.  Across: rows of 512 (B: 256) bytes, one
@@ -154,8 +65,8 @@ struct Transfers {
 
     // Stage kt into LDS from byte address `lds` on; elements past the sum's end read valid memory again.
     __device__ __forceinline__ void issue(const Tile& t, int kt, uint32_t lds, int wave, int lane) const {
-        gchar* A = t.A + (AX ? (size_t)kt * kBK * pitch_a : (size_t)kt * kBK * 2);
-        gchar* B = t.B + (BX ? (size_t)kt * kBK * pitch_b : (size_t)kt * kBK * 2);
+        gchar* Ak = t.A + (AX ? (size_t)kt * kBK * pitch_a : (size_t)kt * kBK * 2);
+        gchar* Bk = t.B + (BX ? (size_t)kt * kBK * pitch_b : (size_t)kt * kBK * 2);
         const int rem = t.nk - kt * kBK;
         uint32_t va[4], vb[2];
 #pragma unroll
@@ -172,203 +83,25 @@ struct Transfers {
             for (int q = 0; q < 2; ++q)
                 vb[q] -= BX ? (uint32_t)max(16 * q + 4 * wave + (lane >> 4) - (rem - 1), 0) * pitch_b : back;
         }
+        base_ready(Ak, Bk);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) to_lds16(A, va[q], lds + (uint32_t)(4 * q + wave) * 1024u);
+        for (int q = 0; q < 4; ++q) to_lds16(Ak, va[q], lds + (uint32_t)(4 * q + wave) * 1024u);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            if (BX || q < nb_mine) to_lds16(B, vb[q], lds + kABytes + (uint32_t)(4 * q + wave) * 1024u);
+            if (BX || q < nb_mine) to_lds16(Bk, vb[q], lds + kABytes + (uint32_t)(4 * q + wave) * 1024u);
     }
 };
 
-// Fragments of a stage: lane l holds row l % 32 of a block, elements 8 * (l /
-// 32) .. + 7 of a step of 16.  Across operands come through the transposing
-// read: of 16 lanes, lane i takes column i of the 4 rows x 16 columns whose 8
-// bytes each lane addresses.
-template <bool X, int PITCH, int NB>
-struct Fragments {
-    uint32_t at[X ? NB : 2];
-
-    __device__ __forceinline__ void init(int first_block, int lane) {
-        if (X) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-                at[i] = (uint32_t)((8 * (lane >> 5) + ((lane & 15) >> 2)) * PITCH +
-                                   ((first_block + i) ^ ((lane >> 2) & 3)) * 64 + ((lane >> 4) & 1) * 32 +
-                                   (lane & 3) * 8);
-        } else {
-            const int r = lane & 31;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                at[s] = (uint32_t)((32 * first_block + r) * 64 + ((2 * s + (lane >> 5)) ^ ((r >> 2) & 3)) * 16);
-        }
-    }
-    __device__ __forceinline__ u32x4 load(lchar* base, int s, int i) const {
-        if constexpr (X) {
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((li16x4*)(base + at[i] + 16 * s * PITCH));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((li16x4*)(base + at[i] + (16 * s + 4) * PITCH));
-            const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
-            return u32x4{l[0], l[1], h[0], h[1]};
-        } else {
-            return *(lu32x4*)(base + at[s] + i * 2048);
-        }
-    }
-};
-
-// Outputs of a tile.  A lane holds row b = lane % 32 of each row block and
-// features 8 * (r / 4) + 4 * (lane / 32) + r % 4 of each feature block; they
-// pass through this wavefront's 6 KB of a free slot and leave as whole row
-// segments of 128 bytes, 16 per lane.  Only this wavefront touches its part and
-// its LDS operations run in order, so no barrier is needed.
-template <Epilogue EPI, int NTB>
-__device__ __forceinline__ void store_tile(const Args& p, const Tile& t, long long seg, int e, f32x16 (&acc)[2][NTB],
-                                           lchar* st, int wave, int lane) {
-    const int nrows = t.nb - t.b0;              // rows of the tile that exist
-    const int f0 = t.a0 + (EPI == kSwigluKeep ? 32 : 64) * wave;
-    const int r8 = lane >> 3, c8 = lane & 7;
-    auto pack = [&](const f32x16& v, int g) {
-        return u32x2{bf16x2_rne(v[4 * g], v[4 * g + 1]), bf16x2_rne(v[4 * g + 2], v[4 * g + 3])};
-    };
-#pragma unroll
-    for (int i = 0; i < NTB; ++i) {
-        const int row0 = 32 * i;
-        if constexpr (EPI == kRows || EPI == kSwigluKeep || EPI == kWeight16) {
-            lchar* wr = st + (lane & 31) * 144 + (lane >> 5) * 8;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) *(lu32x2*)(wr + j * 64 + g * 16) = pack(acc[j][i], g);
-            lanes_exchange();
-            const int f = EPI == kSwigluKeep ? f0 + 8 * (c8 & 3) : f0 + 8 * c8;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int row = row0 + 8 * k + r8;
-                u32x4 v = *(lu32x4*)(st + (8 * k + r8) * 144 + c8 * 16);
-                if (row >= nrows || f >= p.na) continue;
-                if constexpr (EPI == kSwigluKeep) {
-                    *(u32x4*)((uint16_t*)p.out + (size_t)(seg + t.b0 + row) * 2 * p.na + (c8 >> 2) * p.na + f) = v;
-                } else if constexpr (EPI == kRows) {
-                    *(u32x4*)((uint16_t*)p.out + (size_t)(seg + t.b0 + row) * p.na + f) = v;
-                } else {
-                    u32x4* o = (u32x4*)((uint16_t*)p.out + ((size_t)e * p.nb + t.b0 + row) * p.na + f);
-                    *o = v;
-                }
-            }
-            lanes_exchange();
-            if constexpr (EPI == kSwigluKeep) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float a[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float v = acc[0][i][4 * g + r];
-                        a[r] = v * sigmoid(v) * acc[1][i][4 * g + r];
-                    }
-                    *(lu32x2*)(wr + g * 16) = u32x2{bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3])};
-                }
-                lanes_exchange();
-                const int r4 = lane >> 2, c4 = lane & 3, fa = f0 + 8 * c4;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int row = row0 + 16 * k + r4;
-                    const u32x4 v = *(lu32x4*)(st + (16 * k + r4) * 144 + c4 * 16);
-                    if (row < nrows && fa < p.na)
-                        *(u32x4*)(p.out2 + (size_t)(seg + t.b0 + row) * p.na + fa) = v;
-                }
-                lanes_exchange();
-            }
-        } else {
-            // fp32 sums: 16 rows of 64 features at a time
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if ((lane & 31) / 16 == half) {
-                    lchar* wr = st + (lane & 15) * 272 + (lane >> 5) * 16;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            *(lu32x4*)(wr + j * 128 + g * 32) =
-                                u32x4{__float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
-                                      __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3])};
-                }
-                lanes_exchange();
-                if constexpr (EPI == kWeight32) {
-                    const int r16 = lane >> 4, c16 = lane & 15, f = f0 + 4 * c16;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int row = row0 + 16 * half + 4 * k + r16;
-                        const u32x4 w = *(lu32x4*)(st + (4 * k + r16) * 272 + c16 * 16);
-                        float4 v = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]),
-                                               __uint_as_float(w[3]));
-                        if (row >= nrows || f >= p.na) continue;
-                        float4* o = (float4*)((float*)p.out + ((size_t)e * p.nb + t.b0 + row) * p.na + f);
-                        if (p.accumulate) {
-                            const float4 old = *o;
-                            v.x += old.x; v.y += old.y; v.z += old.z; v.w += old.w;
-                        }
-                        *o = v;
-                    }
-                } else if constexpr (EPI == kWeight16Add || EPI == kSwigluGrad) {
-                    const int f = f0 + 8 * c8;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int row = row0 + 16 * half + 8 * k + r8;
-                        const u32x4 lo = *(lu32x4*)(st + (8 * k + r8) * 272 + c8 * 32);
-                        const u32x4 hi = *(lu32x4*)(st + (8 * k + r8) * 272 + c8 * 32 + 16);
-                        if (row >= nrows || f >= p.na) continue;
-                        float v[8];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            v[q] = __uint_as_float(lo[q]);
-                            v[4 + q] = __uint_as_float(hi[q]);
-                        }
-                        if constexpr (EPI == kWeight16Add) {
-                            u32x4* o = (u32x4*)((uint16_t*)p.out + ((size_t)e * p.nb + t.b0 + row) * p.na + f);
-                            u32x4 w = *o;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                w[q] = bf16x2_rne(v[2 * q] + bf16_lo(w[q]), v[2 * q + 1] + bf16_hi(w[q]));
-                            *o = w;
-                        } else {
-                            const size_t at = (size_t)(seg + t.b0 + row) * 2 * p.na + f;
-                            const u32x4 gw = *(const u32x4*)(p.h + at), uw = *(const u32x4*)(p.h + at + p.na);
-                            u32x4 og, ou, oa;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                float dg[2], du[2], a[2];
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    const float g = z ? bf16_hi(gw[q]) : bf16_lo(gw[q]);
-                                    const float u = z ? bf16_hi(uw[q]) : bf16_lo(uw[q]);
-                                    const float s = sigmoid(g), d = v[2 * q + z];
-                                    dg[z] = d * u * s * (1.f + g * (1.f - s));
-                                    du[z] = d * g * s;
-                                    a[z] = g * s * u;
-                                }
-                                og[q] = bf16x2_rne(dg[0], dg[1]);
-                                ou[q] = bf16x2_rne(du[0], du[1]);
-                                oa[q] = bf16x2_rne(a[0], a[1]);
-                            }
-                            *(u32x4*)((uint16_t*)p.out + at) = og;
-                            *(u32x4*)((uint16_t*)p.out + at + p.na) = ou;
-                            *(u32x4*)(p.out2 + (size_t)(seg + t.b0 + row) * p.na + f) = oa;
-                        }
-                    }
-                }
-                lanes_exchange();
-            }
-        }
-    }
-}
-
+// One tile; `seg` (rows) or `e` (weight's gradient) says where its outputs go.
 template <bool AX, bool BX, Epilogue EPI, int NTB>
 __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long seg, int e, lchar* lds, int wave,
                                          int lane) {
     Transfers<AX, BX, EPI == kSwigluKeep> tr;
     tr.init(p, t, NTB, wave, lane);
-    Fragments<AX, kTA * 2, 2> fa;
-    Fragments<BX, kTB * 2, NTB> fb;
-    fa.init(2 * wave, lane);
-    fb.init(0, lane);
+    Fragments<AX, kBK, kTA * 2, 2> fa;
+    Fragments<BX, kBK, kTB * 2, NTB> fb;
+    fa.init(2 * wave, 1, lane);
+    fb.init(0, 1, lane);
     f32x16 acc[2][NTB];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -405,13 +138,9 @@ __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long
             for (int s = 0; s < 2; ++s) {
                 const int left = rem - 16 * s - 8 * (lane >> 5);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t m = left >= 2 * q + 2 ? 0xffffffffu : left == 2 * q + 1 ? 0xffffu : 0u;
+                for (int j = 0; j < 2; ++j) a[s][j] = keep_first(a[s][j], left);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) a[s][j][q] &= m;
-#pragma unroll
-                    for (int i = 0; i < NTB; ++i) b[s][i][q] &= m;
-                }
+                for (int i = 0; i < NTB; ++i) b[s][i] = keep_first(b[s][i], left);
             }
         }
 #pragma unroll
@@ -419,21 +148,31 @@ __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long
 #pragma unroll
             for (int i = 0; i < NTB; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[s][j]),
-                                                                        __builtin_bit_cast(bf16x8, b[s][i]), acc[j][i],
-                                                                        0, 0, 0);
+                for (int j = 0; j < 2; ++j) acc[j][i] = multiply(a[s][j], b[s][i], acc[j][i]);
         slot = slot == 2 ? 0 : slot + 1;
     };
     for (int kt = 0; kt + 1 < n; ++kt) stage(kt, std::false_type{});
     if (n > 0) stage(n - 1, std::true_type{});
     // the slot behind the last stage's was read two stages ago, before a barrier that all have passed
-    store_tile<EPI, NTB>(p, t, seg, e, acc, lds + slot * kSlot + wave * (kSlot / 4), wave, lane);
+    store_tile<EPI, 32, 16>(p, t.a0 + (EPI == kSwigluKeep ? 32 : 64) * wave, t.b0, t.nb - t.b0, 0, 1, seg, e, acc,
+                            lds + slot * kSlot + wave * (kSlot / 4), lane);
 }
 
+// run_tile for as many blocks of 32 rows as the tile has.
 template <bool AX, bool BX, Epilogue EPI>
-__global__ __launch_bounds__(256, 2) void k_grouped(Args p) {
-    constexpr bool WEIGHT = EPI == kWeight16 || EPI == kWeight16Add || EPI == kWeight32;
+__device__ __forceinline__ void run_blocks(const Args& p, const Tile& t, long long seg, int e, lchar* lds, int wave,
+                                           int lane) {
+    switch ((min(t.nb - t.b0, kTB) + 31) / 32) {
+        case 1: run_tile<AX, BX, EPI, 1>(p, t, seg, e, lds, wave, lane); break;
+        case 2: run_tile<AX, BX, EPI, 2>(p, t, seg, e, lds, wave, lane); break;
+        case 3: run_tile<AX, BX, EPI, 3>(p, t, seg, e, lds, wave, lane); break;
+        default: run_tile<AX, BX, EPI, 4>(p, t, seg, e, lds, wave, lane); break;
+    }
+}
+
+// Products of rows: one workgroup per tile.
+template <bool AX, Epilogue EPI>
+__global__ __launch_bounds__(256, 2) void k_grouped_rows(Args p) {
     constexpr int AW = EPI == kSwigluKeep ? kTA / 2 : kTA;     // features of a tile
     __shared__ u32x4 s_ring[kSlots * kSlot / 16];
     __shared__ int s_wave[4];
@@ -442,91 +181,86 @@ __global__ __launch_bounds__(256, 2) void k_grouped(Args p) {
     lchar* lds = (lchar*)(__attribute__((address_space(3))) u32x4*)s_ring;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int ta = (p.na + AW - 1) / AW;
-    // rows: the tiles of rows of every expert, counted by each workgroup
-    int mine[kPerThread], rows[kPerThread], before = 0;
+    // the tiles of rows of every expert, counted by each workgroup
+    int mine[kPerThread], rows[kPerThread], sum = 0;
     const int per = (p.E + 255) / 256;
-    long long total;
-    const int tb = WEIGHT ? (p.nb + kTB - 1) / kTB : 0;
-    if (WEIGHT) {
-        total = (long long)p.E * ta * tb;
-    } else {
-        int sum = 0;
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int e = tid * per + i;
-            long long seg;
-            rows[i] = i < per && e < p.E ? expert_rows(p, e, &seg) : 0;
-            mine[i] = (rows[i] + kTB - 1) / kTB;
-            sum += mine[i];
-        }
-        int run = sum;        // inclusive over the wavefront's lanes
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(run, d);
-            if (lane >= d) run += o;
-        }
-        if (lane == 63) s_wave[wave] = run;
-        __syncthreads();
-        before = run - sum;
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w < wave) before += s_wave[w];
-            all += s_wave[w];
-        }
-        total = (long long)all * ta;
+    for (int i = 0; i < kPerThread; ++i) {
+        const int e = tid * per + i;
+        long long seg;
+        rows[i] = i < per && e < p.E ? expert_rows(p, e, &seg) : 0;
+        mine[i] = (rows[i] + kTB - 1) / kTB;
+        sum += mine[i];
     }
+    int run = sum;            // inclusive over the wavefront's lanes
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 63) s_wave[wave] = run;
+    __syncthreads();
+    int before = run - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += s_wave[w];
+        all += s_wave[w];
+    }
+    const long long total = (long long)all * ta;
     // each XCD takes one contiguous run of the tiles, so that tiles that share rows or weights share an L2
     const int xcd = blockIdx.x % kNxcd;
     const long long hi = total * (xcd + 1) / kNxcd;
     for (long long t = total * xcd / kNxcd + blockIdx.x / kNxcd; t < hi; t += gridDim.x / kNxcd) {
-        int e, nrows;
+        const int u = (int)(t / ta);
+#pragma unroll
+        for (int i = 0, at = before; i < kPerThread; at += mine[i], ++i)
+            if (u >= at && u < at + mine[i]) {
+                s_expert = tid * per + i;
+                s_first = at;
+                s_tiles = mine[i];
+                s_rows = rows[i];
+                s_seg = p.seg_off[tid * per + i];
+            }
+        __syncthreads();
+        const int e = uniform(s_expert), tiles = uniform(s_tiles), nrows = uniform(s_rows);
+        const int at = (int)(t - (long long)uniform(s_first) * ta);
+        const long long seg = (long long)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(s_seg >> 32)) << 32) |
+                                          __builtin_amdgcn_readfirstlane((uint32_t)s_seg));
+        // an expert's rows in tiles of nearly one size, whole blocks of 32; its tiles of rows are neighbours
+        const int blocks = ((nrows + 31) / 32 + tiles - 1) / tiles;
+        Tile tile;
+        tile.a0 = (at / tiles) * AW;
+        tile.b0 = (at % tiles) * blocks * 32;
+        tile.nb = min(nrows, tile.b0 + blocks * 32);
+        tile.nk = p.nk;
+        tile.A = uniform_ptr(p.a + (size_t)e * (EPI == kSwigluKeep ? 2 : 1) * p.na * p.nk);
+        tile.B = uniform_ptr(p.b + (size_t)(seg + tile.b0) * p.nk);
+        run_blocks<AX, false, EPI>(p, tile, seg, e, lds, wave, lane);
+        lds_barrier();        // the slots are free for the next tile
+    }
+}
+
+// Weight's gradient, one workgroup per tile.
+template <Epilogue EPI>
+__global__ __launch_bounds__(256, 2) void k_grouped_weight(Args p) {
+    __shared__ u32x4 s_ring[kSlots * kSlot / 16];
+    lchar* lds = (lchar*)(__attribute__((address_space(3))) u32x4*)s_ring;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int ta = (p.na + kTA - 1) / kTA, tb = (p.nb + kTB - 1) / kTB, each = ta * tb;
+    const long long total = (long long)p.E * each;
+    const int xcd = blockIdx.x % kNxcd;
+    const long long hi = total * (xcd + 1) / kNxcd;
+    for (long long t = total * xcd / kNxcd + blockIdx.x / kNxcd; t < hi; t += gridDim.x / kNxcd) {
+        const int e = (int)(t / each), at = (int)(t - (long long)e * each);
         long long seg;
         Tile tile;
-        if (WEIGHT) {
-            e = (int)(t / ((long long)ta * tb));
-            const int at = (int)(t - (long long)e * ta * tb);
-            nrows = uniform(expert_rows(p, e, &seg));
-            tile.a0 = (at % ta) * AW;
-            tile.b0 = (at / ta) * kTB;
-            tile.nb = p.nb;
-            tile.nk = nrows;
-            if (nrows == 0 && p.accumulate) continue;
-            tile.A = uniform_ptr(p.a + (size_t)seg * p.na);
-            tile.B = uniform_ptr(p.b + (size_t)seg * p.nb);
-        } else {
-            const int u = (int)(t / ta);
-#pragma unroll
-            for (int i = 0, at = before; i < kPerThread; at += mine[i], ++i)
-                if (u >= at && u < at + mine[i]) {
-                    s_expert = tid * per + i;
-                    s_first = at;
-                    s_tiles = mine[i];
-                    s_rows = rows[i];
-                    s_seg = p.seg_off[tid * per + i];
-                }
-            __syncthreads();
-            e = uniform(s_expert);
-            const int tiles = uniform(s_tiles), at = (int)(t - (long long)uniform(s_first) * ta);
-            nrows = uniform(s_rows);
-            seg = s_seg;
-            seg = (long long)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(seg >> 32)) << 32) |
-                              __builtin_amdgcn_readfirstlane((uint32_t)seg));
-            // an expert's rows in tiles of nearly one size, whole blocks of 32; its tiles of rows are neighbours
-            const int blocks = ((nrows + 31) / 32 + tiles - 1) / tiles;
-            tile.a0 = (at / tiles) * AW;
-            tile.b0 = (at % tiles) * blocks * 32;
-            tile.nb = min(nrows, tile.b0 + blocks * 32);
-            tile.nk = p.nk;
-            tile.A = uniform_ptr(p.a + (size_t)e * (EPI == kSwigluKeep ? 2 : 1) * p.na * p.nk);
-            tile.B = uniform_ptr(p.b + (size_t)(seg + tile.b0) * p.nk);
-        }
-        asm volatile("s_nop 4" ::: "memory");   // wait states between readfirstlane and the transfers' base
-        switch ((min(tile.nb - tile.b0, kTB) + 31) / 32) {
-            case 1: run_tile<AX, BX, EPI, 1>(p, tile, seg, e, lds, wave, lane); break;
-            case 2: run_tile<AX, BX, EPI, 2>(p, tile, seg, e, lds, wave, lane); break;
-            case 3: run_tile<AX, BX, EPI, 3>(p, tile, seg, e, lds, wave, lane); break;
-            default: run_tile<AX, BX, EPI, 4>(p, tile, seg, e, lds, wave, lane); break;
-        }
+        tile.nk = expert_rows(p, e, &seg);
+        if (tile.nk == 0 && p.accumulate) continue;
+        tile.a0 = (at % ta) * kTA;
+        tile.b0 = (at / ta) * kTB;
+        tile.nb = p.nb;
+        tile.A = uniform_ptr(p.a + (size_t)seg * p.na);
+        tile.B = uniform_ptr(p.b + (size_t)seg * p.nb);
+        run_blocks<true, true, EPI>(p, tile, 0, e, lds, wave, lane);
         lds_barrier();        // the slots are free for the next tile
     }
 }
@@ -547,42 +281,75 @@ Args make_args(const moe_handle* h) {
     return p;
 }
 
-// Most tiles that the rows can make: each expert's last one may be partial.
-long long row_tiles(const moe_handle* h) {
-    const long long copies = (long long)h->desc.T * h->desc.K;
-    return copies / kTB + (copies < h->desc.E ? copies : h->desc.E);
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+long long copies(const moe_handle* h) { return (long long)h->desc.T * h->desc.K; }
+
+// Which kernel.  The host knows the copies and the experts, not who has how
+// many: rows below are the mean.  Measured in us, this file's kernel (two
+// workgroups of 256 x 128 per CU) against the wide one (one of 256 x 256):
+//   rows, 32 experts, 2048 x 2048: 64 rows each 53 and 61, 128 rows 82 and 67, 512 rows 189 and 169; 256 experts,
+//   7168 x 4096: 64 rows 2970 and 3330, 128 rows 3610 and 3550, 256 rows 5000 and 4730; 16 experts, 1024 x 1024, 256
+//   rows (128 wide tiles for 256 CUs) 23 and 27
+//   weights, 64 experts, 4096 x 7168: 8 rows 620 and 730, 64 rows 760 and 710, 512 rows 2600 and 2120; 32 experts,
+//   1024 x 2048 (1024 wide tiles), 1024 rows 148 and 139; 24 experts, 1048 x 904 (480 wide tiles) 78 and 105
+bool wide_rows(const moe_handle* h, int na, int width, int num_cu) {
+    const long long rows = copies(h) / h->desc.E;
+    return rows >= 96 && h->desc.E * ceil_div(rows, 256) * ceil_div(na, width) >= num_cu;
+}
+bool wide_weight(const moe_handle* h, int na, int nb, int num_cu) {
+    return copies(h) / h->desc.E >= 64 && h->desc.E * ceil_div(na, 256) * ceil_div(nb, 256) >= 4ll * num_cu;
+}
+// Weights that are not read across, streamed for few rows: the expert MLP's FC2
+// kernel, which takes a unit's rows all at once and keeps two stages of weights
+// in registers on their way.  256 experts, 7168 x 4096, against the better of the
+// two above: 16 tokens 1010 and 1100 us, 64 rows each 2740 and 2990, 256 rows
+// 4110 and 4850, 512 rows 8780 and 7610.  Below some hundred MB of weights it
+// has too few units: 32 experts, 2048 x 2048, 1 to 64 rows 47 to 76 and 38 to 72.
+bool stream_weights(const moe_handle* h, int N, int M) {
+    const long long touched = copies(h) < h->desc.E ? copies(h) : h->desc.E;
+    return N % 256 == 0 && M % 128 == 0 && copies(h) <= 320ll * h->desc.E && touched * N * M * 2 > (384ll << 20);
 }
 
 template <bool AX, Epilogue EPI>
-hipError_t launch_rows(const moe_handle* h, const Args& p, hipStream_t s) {
+hipError_t launch_rows(const moe_handle* h, const Args& p, int num_cu, hipStream_t s) {
     constexpr int AW = EPI == kSwigluKeep ? kTA / 2 : kTA;
-    const long long tiles = row_tiles(h) * ((p.na + AW - 1) / AW);
-    if (p.R == 0 || tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL((k_grouped<AX, false, EPI>), dim3(grid_for(tiles)), dim3(256), 0, s, p);
+    if (p.R == 0 || copies(h) == 0) return hipSuccess;
+    if (wide_rows(h, p.na, AW, num_cu)) return launch_wide(EPI, AX, p, num_cu, s);
+    // most tiles that the rows can make: each expert's last one may be partial
+    const long long tiles = copies(h) / kTB + (copies(h) < h->desc.E ? copies(h) : h->desc.E);
+    hipLaunchKernelGGL((k_grouped_rows<AX, EPI>), dim3(grid_for(tiles * ceil_div(p.na, AW))), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <Epilogue EPI>
-void launch_weight(const Args& p, hipStream_t s) {
-    const long long tiles = (long long)p.E * ((p.na + kTA - 1) / kTA) * ((p.nb + kTB - 1) / kTB);
-    hipLaunchKernelGGL((k_grouped<true, true, EPI>), dim3(grid_for(tiles)), dim3(256), 0, s, p);
+hipError_t launch_weight(const moe_handle* h, const Args& p, int num_cu, hipStream_t s) {
+    if (wide_weight(h, p.na, p.nb, num_cu)) return launch_wide(EPI, true, p, num_cu, s);
+    hipLaunchKernelGGL((k_grouped_weight<EPI>), dim3(grid_for(p.E * ceil_div(p.na, kTA) * ceil_div(p.nb, kTB))),
+                       dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_grouped_product(const moe_handle* h, int N, int M, int transpose, const void* rows, const void* w,
-                                  void* out, hipStream_t s) {
+                                  void* out, int num_cu, hipStream_t s) {
+    if (!transpose && stream_weights(h, N, M)) {
+        moe_handle g = *h;     // the same segments, rows of N
+        g.desc.H = N;
+        return launch_gemm_bf16(&g, 1, M, rows, w, out, nullptr, num_cu, s);
+    }
     Args p = make_args(h);
     p.a = (const uint16_t*)w;
     p.b = (const uint16_t*)rows;
     p.out = out;
     p.na = transpose ? M : N;
     p.nk = transpose ? N : M;
-    return transpose ? launch_rows<true, kRows>(h, p, s) : launch_rows<false, kRows>(h, p, s);
+    return transpose ? launch_rows<true, kRows>(h, p, num_cu, s) : launch_rows<false, kRows>(h, p, num_cu, s);
 }
 
 hipError_t launch_grouped_swiglu_keep(const moe_handle* h, int F, const void* rows, const void* w1, void* hout,
-                                      void* act, hipStream_t s) {
+                                      void* act, int num_cu, hipStream_t s) {
     Args p = make_args(h);
     p.a = (const uint16_t*)w1;
     p.b = (const uint16_t*)rows;
@@ -590,11 +357,11 @@ hipError_t launch_grouped_swiglu_keep(const moe_handle* h, int F, const void* ro
     p.out2 = (uint16_t*)act;
     p.na = F;
     p.nk = h->desc.H;
-    return launch_rows<false, kSwigluKeep>(h, p, s);
+    return launch_rows<false, kSwigluKeep>(h, p, num_cu, s);
 }
 
 hipError_t launch_grouped_swiglu_grad(const moe_handle* h, int F, const void* grad_out, const void* w2, const void* hin,
-                                      void* grad_h, void* act, hipStream_t s) {
+                                      void* grad_h, void* act, int num_cu, hipStream_t s) {
     Args p = make_args(h);
     p.a = (const uint16_t*)w2;
     p.b = (const uint16_t*)grad_out;
@@ -603,11 +370,11 @@ hipError_t launch_grouped_swiglu_grad(const moe_handle* h, int F, const void* gr
     p.out2 = (uint16_t*)act;
     p.na = F;
     p.nk = h->desc.H;
-    return launch_rows<true, kSwigluGrad>(h, p, s);
+    return launch_rows<true, kSwigluGrad>(h, p, num_cu, s);
 }
 
 hipError_t launch_grouped_weight_grad(const moe_handle* h, int N, int M, int out_dtype, int accumulate,
-                                      const void* grad, const void* rows, void* out, hipStream_t s) {
+                                      const void* grad, const void* rows, void* out, int num_cu, hipStream_t s) {
     Args p = make_args(h);
     p.a = (const uint16_t*)rows;
     p.b = (const uint16_t*)grad;
@@ -615,10 +382,9 @@ hipError_t launch_grouped_weight_grad(const moe_handle* h, int N, int M, int out
     p.na = M;
     p.nb = N;
     p.accumulate = accumulate;
-    if (out_dtype != MOE_BF16) launch_weight<kWeight32>(p, s);
-    else if (accumulate) launch_weight<kWeight16Add>(p, s);
-    else launch_weight<kWeight16>(p, s);
-    return hipGetLastError();
+    if (out_dtype != MOE_BF16) return launch_weight<kWeight32>(h, p, num_cu, s);
+    if (accumulate) return launch_weight<kWeight16Add>(h, p, num_cu, s);
+    return launch_weight<kWeight16>(h, p, num_cu, s);
 }
 
 }  // namespace moe

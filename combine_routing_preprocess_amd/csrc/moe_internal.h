@@ -121,13 +121,13 @@ hipError_t launch_gate_backward(const moe_handle* h, const float* grad_probs, co
 // products grouped by expert of bf16 rows [R, ..] with weights [E,N,M], the
 // weights' gradients, and the products around SwiGLU in training
 hipError_t launch_grouped_product(const moe_handle* h, int N, int M, int transpose, const void* rows, const void* w,
-                                  void* out, hipStream_t s);
+                                  void* out, int num_cu, hipStream_t s);
 hipError_t launch_grouped_weight_grad(const moe_handle* h, int N, int M, int out_dtype, int accumulate,
-                                      const void* grad, const void* rows, void* out, hipStream_t s);
+                                      const void* grad, const void* rows, void* out, int num_cu, hipStream_t s);
 hipError_t launch_grouped_swiglu_keep(const moe_handle* h, int F, const void* rows, const void* w1, void* hout,
-                                      void* act, hipStream_t s);
+                                      void* act, int num_cu, hipStream_t s);
 hipError_t launch_grouped_swiglu_grad(const moe_handle* h, int F, const void* grad_out, const void* w2,
-                                      const void* hin, void* grad_h, void* act, hipStream_t s);
+                                      const void* hin, void* grad_h, void* act, int num_cu, hipStream_t s);
 // RMS norm of rows and its backward pass
 size_t rms_norm_backward_scratch_bytes(int T, int H);
 hipError_t launch_rms_norm(int T, int H, int x_dtype, int r_dtype, int y_dtype, int w_dtype, const void* x,
