@@ -189,58 +189,66 @@ __device__ __forceinline__ void store_tile(const Args& p, int f0, int b0, int nr
     const long long out_row = (WEIGHT ? (long long)e * p.nb : seg) + b0;
     const uint32_t width = (EPI == kSwigluKeep || EPI == kSwigluGrad ? 2u : 1u) * p.na;
     if constexpr (EPI == kRows || EPI == kSwigluKeep || EPI == kWeight16) {
+        // In the order write, read, write the next, store: a part's stores wait for its reads while the next is on its
+        // way.  kSwigluKeep takes two parts for each: h, then the activations.
+        constexpr int PARTS = 32 / R16, KINDS = EPI == kSwigluKeep ? 2 : 1, N = NTB * PARTS * KINDS;
+        const int f = EPI == kSwigluKeep ? f0 + 8 * (c8 & 3) : f0 + 8 * c8;
+        const uint32_t lane_at = (uint32_t)r8 * width + (uint32_t)(EPI == kSwigluKeep ? (c8 >> 2) * p.na : 0) + f;
+        const int r4 = lane >> 2, fa = f0 + 8 * (lane & 3);
+        auto write = [&](int at) {
+            const int i = at / (PARTS * KINDS), part = at / KINDS % PARTS;
+            lchar* wr = st + (lane & (R16 - 1)) * 144 + (lane >> 5) * 8;
+            if (R16 < 32 && (lane & 31) / R16 != part) return;
+            if (at % KINDS == 0) {
 #pragma unroll
-        for (int i = 0; i < NTB; ++i)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int part = 0; part < 32 / R16; ++part) {
-                const int row0 = 32 * (first + i * step) + part * R16;
-                const bool mine = R16 == 32 || (lane & 31) / R16 == part;
-                lchar* wr = st + (lane & (R16 - 1)) * 144 + (lane >> 5) * 8;
-                if (mine) {
+                    for (int g = 0; g < 4; ++g)
+                        *(lu32x2*)(wr + j * 64 + g * 16) = u32x2{bf16x2_rne(acc[j][i][4 * g], acc[j][i][4 * g + 1]),
+                                                                 bf16x2_rne(acc[j][i][4 * g + 2], acc[j][i][4 * g + 3])};
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                for (int g = 0; g < 4; ++g) {
+                    float a[4];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            *(lu32x2*)(wr + j * 64 + g * 16) =
-                                u32x2{bf16x2_rne(acc[j][i][4 * g], acc[j][i][4 * g + 1]),
-                                      bf16x2_rne(acc[j][i][4 * g + 2], acc[j][i][4 * g + 3])};
-                }
-                lanes_exchange();
-                const int f = EPI == kSwigluKeep ? f0 + 8 * (c8 & 3) : f0 + 8 * c8;
-                const uint32_t lane_at = (uint32_t)r8 * width + (uint32_t)(EPI == kSwigluKeep ? (c8 >> 2) * p.na : 0) + f;
-#pragma unroll
-                for (int k = 0; k < R16 / 8; ++k) {
-                    const u32x4 v = *(lu32x4*)(st + (8 * k + r8) * 144 + c8 * 16);
-                    if (row0 + 8 * k + r8 >= nrows || f >= p.na) continue;
-                    uint16_t* o = (uint16_t*)p.out + (size_t)(out_row + row0 + 8 * k) * width;
-                    if constexpr (EPI == kWeight16) __builtin_nontemporal_store(v, (u32x4*)(o + lane_at));
-                    else *(u32x4*)(o + lane_at) = v;
-                }
-                lanes_exchange();
-                if constexpr (EPI == kSwigluKeep) {
-                    if (mine) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            float a[4];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float v = acc[0][i][4 * g + r];
-                                a[r] = v * sigmoid(v) * acc[1][i][4 * g + r];
-                            }
-                            *(lu32x2*)(wr + g * 16) = u32x2{bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3])};
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = acc[0][i][4 * g + r];
+                        a[r] = v * sigmoid(v) * acc[1][i][4 * g + r];
                     }
-                    lanes_exchange();
-                    const int r4 = lane >> 2, fa = f0 + 8 * (lane & 3);
-#pragma unroll
-                    for (int k = 0; k < R16 / 16; ++k) {
-                        const u32x4 v = *(lu32x4*)(st + (16 * k + r4) * 144 + (lane & 3) * 16);
-                        if (row0 + 16 * k + r4 < nrows && fa < p.na)
-                            *(u32x4*)(p.out2 + (size_t)(out_row + row0 + 16 * k) * p.na + ((uint32_t)r4 * p.na + fa)) = v;
-                    }
-                    lanes_exchange();
+                    *(lu32x2*)(wr + g * 16) = u32x2{bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3])};
                 }
             }
+        };
+        if constexpr (N > 0) write(0);
+#pragma unroll
+        for (int at = 0; at < N; ++at) {
+            const int row0 = 32 * (first + at / (PARTS * KINDS) * step) + at / KINDS % PARTS * R16;
+            lanes_exchange();
+            u32x4 v[R16 / 8];
+            if (at % KINDS == 0) {
+#pragma unroll
+                for (int k = 0; k < R16 / 8; ++k) v[k] = *(lu32x4*)(st + (8 * k + r8) * 144 + c8 * 16);
+            } else {
+#pragma unroll
+                for (int k = 0; k < R16 / 16; ++k) v[k] = *(lu32x4*)(st + (16 * k + r4) * 144 + (lane & 3) * 16);
+            }
+            lanes_exchange();
+            if (at + 1 < N) write(at + 1);
+            if (at % KINDS == 0) {
+#pragma unroll
+                for (int k = 0; k < R16 / 8; ++k) {
+                    if (row0 + 8 * k + r8 >= nrows || f >= p.na) continue;
+                    uint16_t* o = (uint16_t*)p.out + (size_t)(out_row + row0 + 8 * k) * width;
+                    if constexpr (EPI == kWeight16) __builtin_nontemporal_store(v[k], (u32x4*)(o + lane_at));
+                    else *(u32x4*)(o + lane_at) = v[k];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < R16 / 16; ++k)
+                    if (row0 + 16 * k + r4 < nrows && fa < p.na)
+                        *(u32x4*)(p.out2 + (size_t)(out_row + row0 + 16 * k) * p.na + ((uint32_t)r4 * p.na + fa)) = v[k];
+            }
+        }
     } else if constexpr (EPI == kWeight16Add || EPI == kWeight32) {
         const int r16 = lane >> 4, f = f0 + 4 * (lane & 15);
         typedef std::conditional_t<EPI == kWeight32, u32x4, u32x2> Four;   // four elements

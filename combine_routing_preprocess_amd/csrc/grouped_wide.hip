@@ -115,8 +115,7 @@ __device__ __forceinline__ void run_tile(const Args& p, Place t, Transfers<AX, B
             for (int j = 0; j < 2; ++j) acc[j][i] = multiply(a[buf][j], b[buf][i], acc[j][i]);
     };
     // Step s of a stage is loaded while step s - 1 is multiplied; the last one's products follow the next stage's barrier.
-    auto stage = [&](int kt, auto lastc) {
-        constexpr bool LAST = decltype(lastc)::value;
+    auto stage = [&]() {
         lchar* s0 = lds + slot * kSlot;
 #pragma unroll
         for (int s = 0; s < (NTB > 0 ? kBK / 16 : 0); ++s) {
@@ -126,20 +125,11 @@ __device__ __forceinline__ void run_tile(const Args& p, Place t, Transfers<AX, B
             for (int j = 0; j < 2; ++j) a[buf][j] = fa.load(s0, s, j);
 #pragma unroll
             for (int i = 0; i < NTB; ++i) b[buf][i] = fb.load(s0 + kOperand, s, i);
-            if (LAST) {
-                const int left = nk - kt * kBK - 16 * s - 8 * (lane >> 5);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) a[buf][j] = keep_first(a[buf][j], left);
-#pragma unroll
-                for (int i = 0; i < NTB; ++i) b[buf][i] = keep_first(b[buf][i], left);
-            }
             mul(buf ^ 1);
-            if (!LAST) {
 #pragma unroll
-                for (int i = 0; i < 2 * NTB; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                }
+            for (int i = 0; i < 2 * NTB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -161,13 +151,22 @@ __device__ __forceinline__ void run_tile(const Args& p, Place t, Transfers<AX, B
         if (kt > 0) wait_vm<0>();
         lds_barrier();         // stage kt is there, and every wavefront has read stage kt - 1
         tr.issue(kt + 1, base + (slot ^ 1) * kSlot, wave, lane);
-        stage(kt, std::false_type{});
+        stage();
     }
     if (n > 1) wait_vm<0>();
     lds_barrier();
     next(slot ^ 1);            // the next tile's first stage
-    stage(n - 1, std::true_type{});
+    // the last one: as many steps as there are, elements past the sum's end zero in both operands
     mul(1);
+    for (int s = 0, left = nk - (n - 1) * kBK; NTB > 0 && left > 0; ++s, left -= 16) {
+        lchar* s0 = lds + slot * kSlot;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[0][j] = keep_first(fa.load(s0, s, j), left - 8 * (lane >> 5));
+#pragma unroll
+        for (int i = 0; i < NTB; ++i) b[0][i] = keep_first(fb.load(s0 + kOperand, s, i), left - 8 * (lane >> 5));
+        mul(0);
+    }
+    slot ^= 1;
     wait_vm<0>();              // before the stores, so that the next tile waits for none of them
     store();
 }
@@ -261,11 +260,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_grouped_wide(Args p) {
     if (tr.nk > 0) tr.issue(0, base, wave, lane);
     wait_vm<0>();
     while (t < hi) {
-        Place then = cur;
         const long long t2 = t + step;
+        const Place then = t2 < hi ? place(t2) : cur;
         auto next = [&](int sl) {
             if (t2 < hi) {
-                then = place(t2);
                 tr.init(p, then, wave, lane);
                 if (tr.nk > 0) tr.issue(0, base + sl * kSlot, wave, lane);
             }
