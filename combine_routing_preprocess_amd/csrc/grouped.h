@@ -67,13 +67,6 @@ template <int N>
 __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// At most n of this wavefront's transfers in flight.
-__device__ __forceinline__ void wait_transfers(int n) {
-    if (n == 6) wait_vm<6>();
-    else if (n == 5) wait_vm<5>();
-    else if (n == 4) wait_vm<4>();
-    else wait_vm<0>();
-}
 // Workgroup barrier; this wavefront's LDS reads are complete before it
 // arrives, its transfers may be in flight.
 __device__ __forceinline__ void lds_barrier() {

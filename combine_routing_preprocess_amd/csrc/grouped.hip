@@ -17,91 +17,127 @@ using namespace grouped;
 
 namespace {
 
-constexpr int kTA = 256;                    // features of a tile: 64 per wavefront
 constexpr int kTB = 128;                    // rows (weight's gradient: columns of the gradient) of a tile
 constexpr int kBK = 32;                     // sum's elements per stage
-constexpr int kSlots = 3;                   // stages in LDS
-constexpr int kABytes = kTA * kBK * 2, kBBytes = kTB * kBK * 2, kSlot = kABytes + kBBytes;
+constexpr int kBBytes = kTB * kBK * 2;
 constexpr int kPerThread = kMaxE / 256;     // experts whose tiles one thread counts
 
+// A tile's features: 64 for each of FW wavefronts, which share the rows with
+// the other 4 / FW, every other block of 32 each.
+template <int FW>
+struct Geometry {
+    static constexpr int TA = 64 * FW, HALVES = 4 / FW;
+    static constexpr int ABytes = TA * kBK * 2, Slot = ABytes + kBBytes;
+    static constexpr int Slots = FW == 4 ? 3 : 4;                      // stages in LDS: two workgroups per CU
+    static constexpr int R16 = FW == 4 ? 32 : 16, R32 = R16 / 2;       // epilogue rows that fit a quarter of a slot
+    static_assert(R16 * 144 <= Slot / 4 && R32 * 272 <= Slot / 4 && Slots * Slot <= 76 * 1024, "LDS budget");
+};
+
 // A stage's transfers.  Not across: rows of 64 bytes, four chunks of 16, chunk
-// c of row r at place c ^ (r / 4) % 4.  Across: rows of 512 (B: 256) bytes, one
-// per element of the sum, in units of 64 bytes, unit u of row k at place
+// c of row r at place c ^ (r / 4) % 4.  Across: rows of 128 FW (B: 256) bytes,
+// one per element of the sum, in units of 64 bytes, unit u of row k at place
 // u ^ k % 4.  Either way the reads below touch every bank once.
-template <bool AX, bool BX, bool KEEP>
+template <bool AX, bool BX, bool KEEP, int FW>
 struct Transfers {
-    uint32_t a[4], b[2];      // per-lane offsets
+    uint32_t a[FW], b[2];     // per-lane offsets
     int nb_mine;              // B transfers of this wavefront
     uint32_t pitch_a, pitch_b;
 
-    __device__ __forceinline__ void init(const Args& p, const Tile& t, int ntb, int wave, int lane) {
+    // row of an across operand of which this lane fetches a chunk: 1024 / BYTES rows of BYTES bytes per transfer
+    template <int BYTES>
+    static __device__ __forceinline__ int across_row(int q, int wave, int lane) {
+        return (1024 / BYTES) * (4 * q + wave) + lane / (BYTES / 16);
+    }
+    template <int BYTES>
+    static __device__ __forceinline__ int across_chunk(int k, int lane) {
+        return (lane & (BYTES / 16 - 1)) ^ ((k & 3) << 2);
+    }
+
+    __device__ __forceinline__ void init(const Args& p, const Tile& t, int wave, int lane) {
         pitch_a = (uint32_t)(AX ? p.na : t.nk) * 2u;
         pitch_b = (uint32_t)(BX ? p.nb : t.nk) * 2u;
         const uint32_t c4 = (uint32_t)((lane & 3) ^ ((lane >> 4) & 3)) * 16u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < FW; ++q) {
+            const int r = 64 * q + 16 * wave + (lane >> 2);
             if (AX) {
-                const int k = 8 * q + 2 * wave + (lane >> 5), c = (lane & 31) ^ ((k & 3) << 2);
-                a[q] = (uint32_t)k * pitch_a + (uint32_t)min(t.a0 + 8 * c, p.na - 8) * 2u;
+                const int k = across_row<128 * FW>(q, wave, lane);
+                a[q] = (uint32_t)k * pitch_a + (uint32_t)min(t.a0 + 8 * across_chunk<128 * FW>(k, lane), p.na - 8) * 2u;
             } else if (KEEP) {      // rows 64 q .. of the tile: 32 gate features, the same 32 up
-                const int f = min(t.a0 + 32 * q + 16 * (wave & 1) + (lane >> 2), p.na - 1);
-                a[q] = (uint32_t)(f + (wave >> 1) * p.na) * pitch_a + c4;
+                const int f = min(t.a0 + r / 64 * 32 + r % 32, p.na - 1);
+                a[q] = (uint32_t)(f + (r % 64) / 32 * p.na) * pitch_a + c4;
             } else {
-                a[q] = (uint32_t)min(t.a0 + 64 * q + 16 * wave + (lane >> 2), p.na - 1) * pitch_a + c4;
+                a[q] = (uint32_t)min(t.a0 + r, p.na - 1) * pitch_a + c4;
             }
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             if (BX) {
-                const int k = 16 * q + 4 * wave + (lane >> 4), c = (lane & 15) ^ ((k & 3) << 2);
-                b[q] = (uint32_t)k * pitch_b + (uint32_t)min(t.b0 + 8 * c, t.nb - 8) * 2u;
+                const int k = across_row<256>(q, wave, lane);
+                b[q] = (uint32_t)k * pitch_b + (uint32_t)min(t.b0 + 8 * across_chunk<256>(k, lane), t.nb - 8) * 2u;
             } else {
                 b[q] = (uint32_t)min(64 * q + 16 * wave + (lane >> 2), t.nb - t.b0 - 1) * pitch_b + c4;
             }
         }
-        nb_mine = BX ? 2 : (2 * ntb - wave + 3) / 4;
+        nb_mine = BX ? 2 : (2 * ((t.nb - t.b0 + 31) / 32) - wave + 3) / 4;
     }
-    __device__ __forceinline__ int count() const { return 4 + nb_mine; }
+    __device__ __forceinline__ int count() const { return FW + nb_mine; }
 
     // Stage kt into LDS from byte address `lds` on; elements past the sum's end read valid memory again.
     __device__ __forceinline__ void issue(const Tile& t, int kt, uint32_t lds, int wave, int lane) const {
         gchar* Ak = t.A + (AX ? (size_t)kt * kBK * pitch_a : (size_t)kt * kBK * 2);
         gchar* Bk = t.B + (BX ? (size_t)kt * kBK * pitch_b : (size_t)kt * kBK * 2);
         const int rem = t.nk - kt * kBK;
-        uint32_t va[4], vb[2];
+        uint32_t va[FW], vb[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) va[q] = a[q];
+        for (int q = 0; q < FW; ++q) va[q] = a[q];
 #pragma unroll
         for (int q = 0; q < 2; ++q) vb[q] = b[q];
         if (rem < kBK) {
             const uint32_t c = (uint32_t)((lane & 3) ^ ((lane >> 4) & 3));
             const uint32_t back = (int)(8 * c) >= rem ? 16u * c : 0u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                va[q] -= AX ? (uint32_t)max(8 * q + 2 * wave + (lane >> 5) - (rem - 1), 0) * pitch_a : back;
+            for (int q = 0; q < FW; ++q)
+                va[q] -= AX ? (uint32_t)max(across_row<128 * FW>(q, wave, lane) - (rem - 1), 0) * pitch_a : back;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                vb[q] -= BX ? (uint32_t)max(16 * q + 4 * wave + (lane >> 4) - (rem - 1), 0) * pitch_b : back;
+                vb[q] -= BX ? (uint32_t)max(across_row<256>(q, wave, lane) - (rem - 1), 0) * pitch_b : back;
         }
         base_ready(Ak, Bk);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) to_lds16(Ak, va[q], lds + (uint32_t)(4 * q + wave) * 1024u);
+        for (int q = 0; q < FW; ++q) to_lds16(Ak, va[q], lds + (uint32_t)(4 * q + wave) * 1024u);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            if (BX || q < nb_mine) to_lds16(Bk, vb[q], lds + kABytes + (uint32_t)(4 * q + wave) * 1024u);
+            if (BX || q < nb_mine)
+                to_lds16(Bk, vb[q], lds + Geometry<FW>::ABytes + (uint32_t)(4 * q + wave) * 1024u);
     }
 };
 
+// At most n of this wavefront's transfers in flight (fewer where n has no case).
+__device__ __forceinline__ void wait_transfers(int n) {
+    if (n >= 8) wait_vm<8>();
+    else if (n >= 6) wait_vm<6>();
+    else if (n == 5) wait_vm<5>();
+    else if (n == 4) wait_vm<4>();
+    else if (n == 3) wait_vm<3>();
+    else if (n == 2) wait_vm<2>();
+    else wait_vm<0>();
+}
+
 // One tile; `seg` (rows) or `e` (weight's gradient) says where its outputs go.
-template <bool AX, bool BX, Epilogue EPI, int NTB>
+// NTB: blocks of 32 rows of each half.
+template <bool AX, bool BX, Epilogue EPI, int FW, int NTB>
 __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long seg, int e, lchar* lds, int wave,
                                          int lane) {
-    Transfers<AX, BX, EPI == kSwigluKeep> tr;
-    tr.init(p, t, NTB, wave, lane);
-    Fragments<AX, kBK, kTA * 2, 2> fa;
+    using G = Geometry<FW>;
+    constexpr int S = G::Slots;
+    const int fw = wave % FW, half = wave / FW;
+    Transfers<AX, BX, EPI == kSwigluKeep, FW> tr;
+    tr.init(p, t, wave, lane);
+    Fragments<AX, kBK, G::TA * 2, 2> fa;
     Fragments<BX, kBK, kTB * 2, NTB> fb;
-    fa.init(2 * wave, 1, lane);
-    fb.init(0, 1, lane);
+    fa.init(2 * fw, 1, lane);
+    fb.init(half, G::HALVES, lane);
     f32x16 acc[2][NTB];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -112,25 +148,26 @@ __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     const int n = (t.nk + kBK - 1) / kBK;
     int slot = 0;             // of the stage that is multiplied
-    if (n > 0) tr.issue(t, 0, base, wave, lane);
-    if (n > 1) tr.issue(t, 1, base + kSlot, wave, lane);
-    // Stage kt has landed when at most the transfers of stage kt + 1 are in
-    // flight; past the barrier every wavefront's have, and the slot of stage
-    // kt - 1, which all have read, takes stage kt + 2.
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+        if (n > i) tr.issue(t, i, base + i * G::Slot, wave, lane);
+    // Stage kt has landed when at most the transfers of the S - 2 stages after
+    // it are in flight; past the barrier every wavefront's have, and the slot
+    // of stage kt - 1, which all have read, takes stage kt + S - 1.
     auto stage = [&](int kt, auto lastc) {
         constexpr bool LAST = decltype(lastc)::value;
         if (LAST) wait_vm<0>();
-        else wait_transfers(tr.count());
+        else wait_transfers(tr.count() * min(S - 2, n - 1 - kt));
         lds_barrier();
-        if (!LAST && kt + 2 < n) tr.issue(t, kt + 2, base + (slot == 0 ? 2 : slot - 1) * kSlot, wave, lane);
-        lchar* s0 = lds + slot * kSlot;
+        if (!LAST && kt + S - 1 < n) tr.issue(t, kt + S - 1, base + (slot == 0 ? S - 1 : slot - 1) * G::Slot, wave, lane);
+        lchar* s0 = lds + slot * G::Slot;
         u32x4 a[2][2], b[2][NTB];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) a[s][j] = fa.load(s0, s, j);
 #pragma unroll
-            for (int i = 0; i < NTB; ++i) b[s][i] = fb.load(s0 + kABytes, s, i);
+            for (int i = 0; i < NTB; ++i) b[s][i] = fb.load(s0 + G::ABytes, s, i);
         }
         if (LAST) {           // elements past the sum's end become zero in both operands
             const int rem = t.nk - kt * kBK;
@@ -149,32 +186,39 @@ __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long
             for (int i = 0; i < NTB; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[j][i] = multiply(a[s][j], b[s][i], acc[j][i]);
-        slot = slot == 2 ? 0 : slot + 1;
+        slot = slot == S - 1 ? 0 : slot + 1;
     };
     for (int kt = 0; kt + 1 < n; ++kt) stage(kt, std::false_type{});
     if (n > 0) stage(n - 1, std::true_type{});
-    // the slot behind the last stage's was read two stages ago, before a barrier that all have passed
-    store_tile<EPI, 32, 16>(p, t.a0 + (EPI == kSwigluKeep ? 32 : 64) * wave, t.b0, t.nb - t.b0, 0, 1, seg, e, acc,
-                            lds + slot * kSlot + wave * (kSlot / 4), lane);
+    // the slot behind the last stage's was read S - 1 stages ago, before a barrier that all have passed
+    store_tile<EPI, G::R16, G::R32>(p, t.a0 + (EPI == kSwigluKeep ? 32 : 64) * fw, t.b0, t.nb - t.b0, half, G::HALVES,
+                                    seg, e, acc, lds + slot * G::Slot + wave * (G::Slot / 4), lane);
 }
 
 // run_tile for as many blocks of 32 rows as the tile has.
-template <bool AX, bool BX, Epilogue EPI>
+template <bool AX, bool BX, Epilogue EPI, int FW>
 __device__ __forceinline__ void run_blocks(const Args& p, const Tile& t, long long seg, int e, lchar* lds, int wave,
                                            int lane) {
-    switch ((min(t.nb - t.b0, kTB) + 31) / 32) {
-        case 1: run_tile<AX, BX, EPI, 1>(p, t, seg, e, lds, wave, lane); break;
-        case 2: run_tile<AX, BX, EPI, 2>(p, t, seg, e, lds, wave, lane); break;
-        case 3: run_tile<AX, BX, EPI, 3>(p, t, seg, e, lds, wave, lane); break;
-        default: run_tile<AX, BX, EPI, 4>(p, t, seg, e, lds, wave, lane); break;
+    const int blocks = (min(t.nb - t.b0, kTB) + 31) / 32;
+    if constexpr (FW == 4) {
+        switch (blocks) {
+            case 1: run_tile<AX, BX, EPI, FW, 1>(p, t, seg, e, lds, wave, lane); break;
+            case 2: run_tile<AX, BX, EPI, FW, 2>(p, t, seg, e, lds, wave, lane); break;
+            case 3: run_tile<AX, BX, EPI, FW, 3>(p, t, seg, e, lds, wave, lane); break;
+            default: run_tile<AX, BX, EPI, FW, 4>(p, t, seg, e, lds, wave, lane); break;
+        }
+    } else {
+        if (blocks <= 2) run_tile<AX, BX, EPI, FW, 1>(p, t, seg, e, lds, wave, lane);
+        else run_tile<AX, BX, EPI, FW, 2>(p, t, seg, e, lds, wave, lane);
     }
 }
 
 // Products of rows: one workgroup per tile.
-template <bool AX, Epilogue EPI>
+template <bool AX, Epilogue EPI, int FW>
 __global__ __launch_bounds__(256, 2) void k_grouped_rows(Args p) {
-    constexpr int AW = EPI == kSwigluKeep ? kTA / 2 : kTA;     // features of a tile
-    __shared__ u32x4 s_ring[kSlots * kSlot / 16];
+    using G = Geometry<FW>;
+    constexpr int AW = EPI == kSwigluKeep ? G::TA / 2 : G::TA;     // features of a tile
+    __shared__ u32x4 s_ring[G::Slots * G::Slot / 16];
     __shared__ int s_wave[4];
     __shared__ int s_expert, s_first, s_tiles, s_rows;
     __shared__ long long s_seg;
@@ -234,18 +278,19 @@ __global__ __launch_bounds__(256, 2) void k_grouped_rows(Args p) {
         tile.nk = p.nk;
         tile.A = uniform_ptr(p.a + (size_t)e * (EPI == kSwigluKeep ? 2 : 1) * p.na * p.nk);
         tile.B = uniform_ptr(p.b + (size_t)(seg + tile.b0) * p.nk);
-        run_blocks<AX, false, EPI>(p, tile, seg, e, lds, wave, lane);
+        run_blocks<AX, false, EPI, FW>(p, tile, seg, e, lds, wave, lane);
         lds_barrier();        // the slots are free for the next tile
     }
 }
 
 // Weight's gradient, one workgroup per tile.
-template <Epilogue EPI>
+template <Epilogue EPI, int FW>
 __global__ __launch_bounds__(256, 2) void k_grouped_weight(Args p) {
-    __shared__ u32x4 s_ring[kSlots * kSlot / 16];
+    using G = Geometry<FW>;
+    __shared__ u32x4 s_ring[G::Slots * G::Slot / 16];
     lchar* lds = (lchar*)(__attribute__((address_space(3))) u32x4*)s_ring;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int ta = (p.na + kTA - 1) / kTA, tb = (p.nb + kTB - 1) / kTB, each = ta * tb;
+    const int ta = (p.na + G::TA - 1) / G::TA, tb = (p.nb + kTB - 1) / kTB, each = ta * tb;
     const long long total = (long long)p.E * each;
     const int xcd = blockIdx.x % kNxcd;
     const long long hi = total * (xcd + 1) / kNxcd;
@@ -255,12 +300,12 @@ __global__ __launch_bounds__(256, 2) void k_grouped_weight(Args p) {
         Tile tile;
         tile.nk = expert_rows(p, e, &seg);
         if (tile.nk == 0 && p.accumulate) continue;
-        tile.a0 = (at % ta) * kTA;
+        tile.a0 = (at % ta) * G::TA;
         tile.b0 = (at / ta) * kTB;
         tile.nb = p.nb;
         tile.A = uniform_ptr(p.a + (size_t)seg * p.na);
         tile.B = uniform_ptr(p.b + (size_t)seg * p.nb);
-        run_blocks<true, true, EPI>(p, tile, 0, e, lds, wave, lane);
+        run_blocks<true, true, EPI, FW>(p, tile, 0, e, lds, wave, lane);
         lds_barrier();        // the slots are free for the next tile
     }
 }
@@ -306,27 +351,34 @@ bool wide_weight(const moe_handle* h, int na, int nb, int num_cu) {
 // two above: 16 tokens 1010 and 1100 us, 64 rows each 2740 and 2990, 256 rows
 // 4110 and 4850, 512 rows 8780 and 7610.  Below some hundred MB of weights it
 // has too few units: 32 experts, 2048 x 2048, 1 to 64 rows 47 to 76 and 38 to 72.
-bool stream_weights(const moe_handle* h, int N, int M) {
+bool stream_weights(const moe_handle* h, int N, int M, int num_cu) {
     const long long touched = copies(h) < h->desc.E ? copies(h) : h->desc.E;
-    return N % 256 == 0 && M % 128 == 0 && copies(h) <= 320ll * h->desc.E && touched * N * M * 2 > (384ll << 20);
+    return N % 256 == 0 && M % 128 == 0 && copies(h) <= 320ll * h->desc.E && touched * N * M * 2 > (384ll << 20) &&
+           touched * (N / 256) >= 2ll * num_cu;
 }
 
 template <bool AX, Epilogue EPI>
 hipError_t launch_rows(const moe_handle* h, const Args& p, int num_cu, hipStream_t s) {
-    constexpr int AW = EPI == kSwigluKeep ? kTA / 2 : kTA;
+    constexpr int AW = EPI == kSwigluKeep ? 128 : 256;
     if (p.R == 0 || copies(h) == 0) return hipSuccess;
     if (wide_rows(h, p.na, AW, num_cu)) return launch_wide(EPI, AX, p, num_cu, s);
     // most tiles that the rows can make: each expert's last one may be partial
     const long long tiles = copies(h) / kTB + (copies(h) < h->desc.E ? copies(h) : h->desc.E);
-    hipLaunchKernelGGL((k_grouped_rows<AX, EPI>), dim3(grid_for(tiles * ceil_div(p.na, AW))), dim3(256), 0, s, p);
+    if (tiles * ceil_div(p.na, AW) < num_cu)
+        hipLaunchKernelGGL((k_grouped_rows<AX, EPI, 2>), dim3(grid_for(tiles * ceil_div(p.na, AW / 2))), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((k_grouped_rows<AX, EPI, 4>), dim3(grid_for(tiles * ceil_div(p.na, AW))), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <Epilogue EPI>
 hipError_t launch_weight(const moe_handle* h, const Args& p, int num_cu, hipStream_t s) {
     if (wide_weight(h, p.na, p.nb, num_cu)) return launch_wide(EPI, true, p, num_cu, s);
-    hipLaunchKernelGGL((k_grouped_weight<EPI>), dim3(grid_for(p.E * ceil_div(p.na, kTA) * ceil_div(p.nb, kTB))),
-                       dim3(256), 0, s, p);
+    const long long tiles = p.E * ceil_div(p.nb, kTB);
+    if (tiles * ceil_div(p.na, 256) < 2ll * num_cu)
+        hipLaunchKernelGGL((k_grouped_weight<EPI, 2>), dim3(grid_for(tiles * ceil_div(p.na, 128))), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((k_grouped_weight<EPI, 4>), dim3(grid_for(tiles * ceil_div(p.na, 256))), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -334,7 +386,7 @@ hipError_t launch_weight(const moe_handle* h, const Args& p, int num_cu, hipStre
 
 hipError_t launch_grouped_product(const moe_handle* h, int N, int M, int transpose, const void* rows, const void* w,
                                   void* out, int num_cu, hipStream_t s) {
-    if (!transpose && stream_weights(h, N, M)) {
+    if (!transpose && stream_weights(h, N, M, num_cu)) {
         moe_handle g = *h;     // the same segments, rows of N
         g.desc.H = N;
         return launch_gemm_bf16(&g, 1, M, rows, w, out, nullptr, num_cu, s);
