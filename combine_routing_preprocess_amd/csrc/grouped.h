@@ -108,7 +108,7 @@ struct Tile {
 // so that each read touches every bank once.  Blocks first, first + step, ...
 template <bool X, int BK, int PITCH, int NB>
 struct Fragments {
-    uint32_t at[X ? NB : BK / 16];
+    uint32_t at[X ? NB : 1];
     int stride;
 
     __device__ __forceinline__ void init(int first, int step, int lane) {
@@ -121,12 +121,10 @@ struct Fragments {
                                            (lane & 3) * 8);
         } else {
             const int r = lane & 31;
-#pragma unroll
-            for (int s = 0; s < BK / 16; ++s)
-                at[X ? 0 : s] = (uint32_t)((32 * first + r) * BK * 2 +
-                                           ((2 * s + (lane >> 5)) ^ ((r / (128 / BK)) & (BK / 8 - 1))) * 16);
+            at[0] = (uint32_t)((32 * first + r) * BK * 2 + ((lane >> 5) ^ ((r / (128 / BK)) & (BK / 8 - 1))) * 16);
         }
     }
+    // Block i of step s.  Not across, chunk 2 s + l / 32 lies where chunk l / 32 does, with the bits of 2 s flipped.
     __device__ __forceinline__ u32x4 load(lchar* base, int s, int i) const {
         if constexpr (X) {
             const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((li16x4*)(base + at[i] + 16 * s * PITCH));
@@ -134,7 +132,7 @@ struct Fragments {
             const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
             return u32x4{l[0], l[1], h[0], h[1]};
         } else {
-            return *(lu32x4*)(base + at[s] + i * stride);
+            return *(lu32x4*)(base + (at[0] ^ (uint32_t)(32 * s)) + i * stride);
         }
     }
 };

@@ -151,45 +151,52 @@ __device__ __forceinline__ void run_tile(const Args& p, const Tile& t, long long
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
         if (n > i) tr.issue(t, i, base + i * G::Slot, wave, lane);
+    u32x4 a[2][2] = {}, b[2][NTB] = {};
+    auto load = [&](lchar* s0, int s, int buf) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[buf][j] = fa.load(s0, s, j);
+#pragma unroll
+        for (int i = 0; i < NTB; ++i) b[buf][i] = fb.load(s0 + G::ABytes, s, i);
+    };
+    auto mul = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < NTB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[j][i] = multiply(a[buf][j], b[buf][i], acc[j][i]);
+    };
     // Stage kt has landed when at most the transfers of the S - 2 stages after
     // it are in flight; past the barrier every wavefront's have, and the slot
-    // of stage kt - 1, which all have read, takes stage kt + S - 1.
-    auto stage = [&](int kt, auto lastc) {
-        constexpr bool LAST = decltype(lastc)::value;
-        if (LAST) wait_vm<0>();
-        else wait_transfers(tr.count() * min(S - 2, n - 1 - kt));
+    // of stage kt - 1, which all have read, takes stage kt + S - 1.  A step is
+    // loaded while the one before it is multiplied; a stage's last products
+    // follow the next stage's barrier.
+    for (int kt = 0; kt + 1 < n; ++kt) {
+        wait_transfers(tr.count() * min(S - 2, n - 1 - kt));
         lds_barrier();
-        if (!LAST && kt + S - 1 < n) tr.issue(t, kt + S - 1, base + (slot == 0 ? S - 1 : slot - 1) * G::Slot, wave, lane);
+        if (kt + S - 1 < n) tr.issue(t, kt + S - 1, base + (slot == 0 ? S - 1 : slot - 1) * G::Slot, wave, lane);
         lchar* s0 = lds + slot * G::Slot;
-        u32x4 a[2][2], b[2][NTB];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) a[s][j] = fa.load(s0, s, j);
-#pragma unroll
-            for (int i = 0; i < NTB; ++i) b[s][i] = fb.load(s0 + G::ABytes, s, i);
-        }
-        if (LAST) {           // elements past the sum's end become zero in both operands
-            const int rem = t.nk - kt * kBK;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int left = rem - 16 * s - 8 * (lane >> 5);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) a[s][j] = keep_first(a[s][j], left);
-#pragma unroll
-                for (int i = 0; i < NTB; ++i) b[s][i] = keep_first(b[s][i], left);
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < NTB; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[j][i] = multiply(a[s][j], b[s][i], acc[j][i]);
+        load(s0, 0, 0);
+        mul(1);
+        __builtin_amdgcn_sched_barrier(0);
+        load(s0, 1, 1);
+        mul(0);
+        __builtin_amdgcn_sched_barrier(0);
         slot = slot == S - 1 ? 0 : slot + 1;
-    };
-    for (int kt = 0; kt + 1 < n; ++kt) stage(kt, std::false_type{});
-    if (n > 0) stage(n - 1, std::true_type{});
+    }
+    if (n > 0) {
+        // the last one: as many steps as there are, elements past the sum's end zero in both operands
+        wait_vm<0>();
+        lds_barrier();
+        mul(1);
+        for (int s = 0, left = t.nk - (n - 1) * kBK; left > 0; ++s, left -= 16) {
+            load(lds + slot * G::Slot, s, 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) a[0][j] = keep_first(a[0][j], left - 8 * (lane >> 5));
+#pragma unroll
+            for (int i = 0; i < NTB; ++i) b[0][i] = keep_first(b[0][i], left - 8 * (lane >> 5));
+            mul(0);
+        }
+        slot = slot == S - 1 ? 0 : slot + 1;
+    }
     // the slot behind the last stage's was read S - 1 stages ago, before a barrier that all have passed
     store_tile<EPI, G::R16, G::R32>(p, t.a0 + (EPI == kSwigluKeep ? 32 : 64) * fw, t.b0, t.nb - t.b0, half, G::HALVES,
                                     seg, e, acc, lds + slot * G::Slot + wave * (G::Slot / 4), lane);
