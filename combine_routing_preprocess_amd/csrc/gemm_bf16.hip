@@ -821,8 +821,8 @@ __global__ __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             int m = 0;
             if (e < E) {
                 const long long so = seg_off[e];
-                long long mm = so < R ? (long long)kept[e] : 0;
-                if (so + mm > R) mm = R - so;
+                long long mm = so < R ? (long long)kept[e] : 0;   // a segment may begin past the end
+                if (mm > 0 && so + mm > R) mm = R - so;
                 m = (int)mm;
             }
             // segments of 257..320 rows take BIG_BLOCKS-block units (one pass)
