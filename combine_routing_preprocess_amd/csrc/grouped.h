@@ -79,8 +79,8 @@ __device__ __forceinline__ void lanes_exchange() { asm volatile("" ::: "memory")
 
 __device__ __forceinline__ int expert_rows(const Args& p, int e, long long* seg) {
     const long long so = p.seg_off[e];
-    long long m = so < p.R ? (long long)p.kept[e] : 0;
-    if (so + m > p.R) m = p.R - so;
+    long long m = so < p.R ? (long long)p.kept[e] : 0;   // a segment may begin past the end
+    if (m > 0 && so + m > p.R) m = p.R - so;
     *seg = so;
     return (int)m;
 }

@@ -27,3 +27,28 @@ def test_grouped_mlp(out_rows):
             _, _, y, dy = _keep_reference(c, x, w1, w2, F, e)
             _within(out[r.to(DEV)], y, dy, ("y", BF, e))
     assert bool((out[c.R:] == 7.0).all())
+
+
+@pytest.mark.parametrize("out_rows", [1, 40, 100, 128])
+@pytest.mark.parametrize("N,M", [(72, 136), (8328, 2832)])
+def test_grouped_products(out_rows, N, M):
+    """The small tiles, and with 8328 x 2832 the wide ones of the weights' gradients."""
+    log("grouped products, rows past the end", out_rows, N, M)
+    c = Case(COUNTS, out_rows=out_rows, seed=7 + out_rows)
+    x, g, w = c.rows(M).to(DEV), c.rows(N).to(DEV), c.weight(N, M).to(DEV)
+    y = torch.full((c.R + 64, N), 7.0, dtype=BF, device=DEV)
+    gx = torch.full((c.R + 64, M), 7.0, dtype=BF, device=DEV)
+    c.d.grouped_product(x, w, out=y[:c.R])
+    c.d.grouped_product(g, w, transpose=True, out=gx[:c.R])
+    gw = c.d.grouped_weight_grad(g, x, out_dtype=F32)
+    more = c.d.grouped_weight_grad(g, x, out=torch.ones_like(gw), accumulate=True)
+    torch.cuda.synchronize()
+    for e, r in enumerate(c.rows_of):
+        r = r.to(DEV)
+        we, xe, ge = w[e].double(), x[r].double(), g[r].double()
+        pairs = [(y[r], _product(xe, we.T), BF), (gx[r], _product(ge, we), BF), (gw[e], _product(ge.T, xe), F32)]
+        want, tol = _product(ge.T, xe)
+        pairs.append((more[e], (want + 1, tol + 2.0 ** -24 * (want.abs() + 1 + tol)), F32))
+        for got, (want, tol), t in pairs:
+            _within(got, want.cpu(), tol.cpu(), (e, t))
+    assert bool((y[c.R:] == 7.0).all()) and bool((gx[c.R:] == 7.0).all())
