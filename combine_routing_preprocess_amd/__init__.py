@@ -1,4 +1,4 @@
-"""MI355X-native MoE layer hot path: layer norm -> gate -> routing
+"""MI355X-native MoE layer hot path: layer or RMS norm -> gate -> routing
 preprocessing -> dispatch-permute -> grouped SwiGLU MLP -> combine-unpermute.
 
 Every step runs in the hand-written HIP kernels of ``libmoe_route.so``
