@@ -369,6 +369,17 @@ bool wide_rows(const moe_handle* h, int na, int width, int num_cu) {
 bool wide_weight(const moe_handle* h, int na, int nb, int num_cu) {
     return copies(h) / h->desc.E >= 64 && h->desc.E * ceil_div(na, 256) * ceil_div(nb, 256) >= 4ll * num_cu;
 }
+// Whether tiles of 128 features take `tiles` of 256 features more evenly: two
+// workgroups per CU work through them in rounds, and a round of the smaller
+// ones takes half the time.  Worth it up to two rounds.  us of the smaller and
+// the larger tiles: 16 experts, 1024 x 1024, 64 tokens 13 and 17, 512 tokens 15
+// and 23; 64 experts, 4096 x 4096, 16 rows 89 and 94; one token, 8 experts of
+// 7168 x 4096, 85 and 138; but 32 experts, 2048 x 2048, 64 rows each (one round of
+// 384 larger tiles, two of the smaller) 61 and 53.
+bool narrow(long long tiles, int features, int width, int num_cu) {
+    const long long wide = tiles * ceil_div(features, width), small = tiles * ceil_div(features, width / 2);
+    return wide < 4ll * num_cu && ceil_div(small, 2 * num_cu) < 2 * ceil_div(wide, 2 * num_cu);
+}
 // Weights that are not read across, streamed for few rows: the expert MLP's FC2
 // kernel, which takes a unit's rows all at once and keeps two stages of weights
 // in registers on their way.  256 experts, 7168 x 4096, against the better of the
@@ -388,7 +399,7 @@ hipError_t launch_rows(const moe_handle* h, const Args& p, int num_cu, hipStream
     if (wide_rows(h, p.na, AW, num_cu)) return launch_wide(EPI, AX, p, num_cu, s);
     // most tiles that the rows can make: each expert's last one may be partial
     const long long tiles = copies(h) / kTB + (copies(h) < h->desc.E ? copies(h) : h->desc.E);
-    if (tiles * ceil_div(p.na, AW) < num_cu)
+    if (narrow(tiles, p.na, AW, num_cu))
         hipLaunchKernelGGL((k_grouped_rows<AX, EPI, 2>), dim3(grid_for(tiles * ceil_div(p.na, AW / 2))), dim3(256), 0, s, p);
     else
         hipLaunchKernelGGL((k_grouped_rows<AX, EPI, 4>), dim3(grid_for(tiles * ceil_div(p.na, AW))), dim3(256), 0, s, p);
@@ -399,7 +410,7 @@ template <Epilogue EPI>
 hipError_t launch_weight(const moe_handle* h, const Args& p, int num_cu, hipStream_t s) {
     if (wide_weight(h, p.na, p.nb, num_cu)) return launch_wide(EPI, true, p, num_cu, s);
     const long long tiles = p.E * ceil_div(p.nb, kTB);
-    if (tiles * ceil_div(p.na, 256) < 2ll * num_cu)
+    if (narrow(tiles, p.na, 256, num_cu))
         hipLaunchKernelGGL((k_grouped_weight<EPI, 2>), dim3(grid_for(tiles * ceil_div(p.na, 128))), dim3(256), 0, s, p);
     else
         hipLaunchKernelGGL((k_grouped_weight<EPI, 4>), dim3(grid_for(tiles * ceil_div(p.na, 256))), dim3(256), 0, s, p);

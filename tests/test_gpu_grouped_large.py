@@ -80,6 +80,35 @@ def test_mlp_both_ways(F):
             _check(got, bound, (name, BF, e))
 
 
+@pytest.mark.parametrize("dtype,accumulate", [(BF, False), (BF, True), (F32, False), (F32, True)])
+def test_mlp_of_many_experts_with_few_rows(dtype, accumulate):
+    """More than two rounds of tiles of 256 features, too few rows for the wide ones."""
+    H, F = 72, 3592
+    counts = [(i * 37) % 61 if i % 5 else 0 for i in range(63)] + [300]
+    log("mlp of many experts", dtype, accumulate)
+    c = Case(counts, H=H, pad=4, seed=17, extra_empty=0)
+    x, gy, h = c.rows(H).to(DEV), c.rows(H).to(DEV), c.rows(2 * F).to(DEV)
+    w1, w2 = c.weight(2 * F, H).to(DEV), c.weight(H, F).to(DEV)
+    y, kept = c.d.grouped_mlp_keep(x, w1, w2)
+    before = [torch.randn(w.shape, device=DEV).to(dtype) for w in (w1, w2)]
+    grads = [b.clone() for b in before]
+    gx, _, _ = c.d.grouped_mlp_backward(gy, x, h, w1, w2, grad_w1=grads[0], grad_w2=grads[1], accumulate=accumulate)
+    torch.cuda.synchronize()
+    for e, rows in enumerate(c.rows_of):
+        r = rows.to(DEV)
+        c.rows_of[e] = r
+        hw, dh, yw, dy = _keep_reference(c, x, w1, w2, F, e)
+        _check(kept[r], (hw, dh), ("h", BF, e))
+        _check(y[r], (yw, dy), ("y", BF, e))
+        rx, *weights = _backward_reference(gy[r], x[r], h[r], w1[e], w2[e], F)
+        _check(gx[r], rx, ("grad_perm", BF, e))
+        for got, old, (want, tol) in zip(grads, before, weights):
+            if accumulate:
+                want = want + old[e].double()
+                tol = tol + 2.0 ** -24 * (want.abs() + tol)
+            _check(got[e], (want, tol), ("weight", dtype, e))
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 5, 2, 0, 1, 3, 300], [320] * 8, [0] * 7 + [2000]])
 def test_streamed_weights(counts):
     """Half a gigabyte of weights, rows from one to many: the kernel that streams them."""
