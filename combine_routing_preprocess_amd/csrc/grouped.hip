@@ -334,7 +334,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_weight(Args p) {
     }
 }
 
-constexpr long long kMaxGrid = 1 << 20;   // workgroups; more tiles than that are walked
+constexpr long long kMaxGrid = 1 << 16;   // workgroups; more tiles than that are walked
 
 unsigned grid_for(long long tiles) {
     const long long g = (tiles + kNxcd - 1) / kNxcd * kNxcd;

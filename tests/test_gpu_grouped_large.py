@@ -109,6 +109,50 @@ def test_mlp_of_many_experts_with_few_rows(dtype, accumulate):
             _check(got[e], (want, tol), ("weight", dtype, e))
 
 
+def _within_on_gpu(got, want_tol):
+    """_check's bound without its copies to the host, as a tensor."""
+    want, tol = want_tol
+    tol = tol + (2.0 ** -8 if got.dtype == BF else 2.0 ** -24) * (want.abs() + tol) + 1e-37
+    return ((got.double() - want).abs() <= tol).all()
+
+
+def test_product_of_more_tiles_than_workgroups():
+    """Some 80 thousand tiles: a workgroup takes one after the other, of several experts."""
+    counts, N, M = [(i * 37) % 21 for i in range(1023)] + [200], 8, 20488
+    log("more product tiles than workgroups")
+    c = Case(counts, pad=4, seed=23, extra_empty=0)
+    x, w = c.rows(N).to(DEV), torch.empty((c.E, N, M), dtype=BF, device=DEV).normal_(0, N ** -0.5)
+    out = torch.full((c.R, M), 7.0, dtype=BF, device=DEV)
+    c.d.grouped_product(x, w, transpose=True, out=out)
+    ok = [_within_on_gpu(out[r.to(DEV)], _product(x[r.to(DEV)].double(), w[e].double()))
+          for e, r in enumerate(c.rows_of)]
+    torch.cuda.synchronize()
+    assert [e for e, good in enumerate(ok) if not bool(good)] == []
+    assert bool((out[~c.live.to(DEV)] == 7.0).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_grad_of_more_tiles_than_workgroups(accumulate):
+    """Some 92 thousand tiles, those of experts without rows between the others."""
+    counts, N, M = [(i * 37) % 21 for i in range(1023)] + [200], 2312, 1032
+    log("more weight tiles than workgroups", accumulate)
+    c = Case(counts, pad=4, seed=29, extra_empty=0)
+    g, x = c.rows(N).to(DEV), c.rows(M).to(DEV)
+    before = torch.empty((c.E, N, M), dtype=BF, device=DEV).normal_(0, 4)
+    out = before.clone()
+    c.d.grouped_weight_grad(g, x, out=out, accumulate=accumulate)
+    ok = []
+    for e, r in enumerate(c.rows_of):
+        r = r.to(DEV)
+        want, tol = _product(g[r].double().T, x[r].double())
+        if accumulate:
+            want = want + before[e].double()
+            tol = tol + 2.0 ** -24 * (want.abs() + tol)
+        ok.append(_within_on_gpu(out[e], (want, tol)))
+    torch.cuda.synchronize()
+    assert [e for e, good in enumerate(ok) if not bool(good)] == []
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 5, 2, 0, 1, 3, 300], [320] * 8, [0] * 7 + [2000]])
 def test_streamed_weights(counts):
     """Half a gigabyte of weights, rows from one to many: the kernel that streams them."""
