@@ -892,7 +892,8 @@ class Dispatcher:
                          out: Optional[torch.Tensor] = None):
         """grouped_mlp with bf16 weights (H and F multiples of 8) for a training
         step: (out [R,H], h [R,2F]), with h, FC1's pre-activations, for
-        grouped_mlp_backward.  ``scratch`` is grouped_mlp's."""
+        grouped_mlp_backward.  The activations are rounded to bf16 once between
+        the two products, as in grouped_mlp.  ``scratch`` is grouped_mlp's."""
         F = self._check_mlp_pair(w1, w2)
         _check_rows(perm, "perm", (self.R, self.H), _BF16)
         if h is None:
@@ -935,7 +936,9 @@ class Dispatcher:
         combine_backward gives it): (grad_perm [R,H], as dispatch_backward
         takes it, grad_w1, grad_w2), the last two of ``grad_dtype`` (bf16 or
         fp32) or of the type of the tensors given; with ``accumulate`` they are
-        added to those.  None without ``want_rows`` / ``want_weights``."""
+        added to those.  None without ``want_rows`` / ``want_weights``.  The
+        activations and h's gradient, operands of the three products, are
+        rounded to bf16 once, whatever the type of the gradients."""
         F = self._check_mlp_pair(w1, w2)
         _check_rows(grad_out, "grad_out", (self.R, self.H), _BF16)
         _check_rows(perm, "perm", (self.R, self.H), _BF16)
