@@ -498,7 +498,8 @@ class Dispatcher:
             if out_scales is None:
                 out_scales = torch.empty((self.R, self.H // 128), dtype=torch.float32, device=self.device)
             self._dev(out_scales, "out_scales")
-            _need(tuple(out_scales.shape) == (self.R, self.H // 128), "out_scales must be [R, H/128]")
+            _need(out_scales.dtype == torch.float32 and tuple(out_scales.shape) == (self.R, self.H // 128),
+                  "out_scales must be float32 [R, H/128]")
         return out, out_scales
 
     def _check_x(self, x):
