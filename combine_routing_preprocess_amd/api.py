@@ -489,7 +489,8 @@ class Dispatcher:
         if out is None:
             out = torch.empty((self.R, self.H), dtype=x.dtype, device=self.device)
         self._dev(out, "out")
-        _need(out.dtype == x.dtype and tuple(out.shape) == (self.R, self.H), "out must be [R,H] like x")
+        _need((out.dtype == x.dtype or (x.dtype in _FP8_DTYPES and out.dtype in _FP8_DTYPES))
+              and tuple(out.shape) == (self.R, self.H), "out must be [R,H] like x")
         if self.payload == A.FP8E4M3_B128:
             _need(x_scales is not None, "fp8 payload needs x_scales")
             self._dev(x_scales, "x_scales")
