@@ -8,6 +8,7 @@ device value back to the host.
 from __future__ import annotations
 
 import ctypes as C
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -80,6 +81,13 @@ def _check_rows(t, name, shape, dtypes):
                          f"{list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _check_aligned(**tensors):
+    """The calls' own condition on addresses, for checks ahead of them."""
+    for name, t in tensors.items():
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{name} must start at a multiple of 16 bytes")
 
 
 def _check_current_device(tensors):
@@ -427,6 +435,26 @@ class Dispatcher:
         if score not in _SCORE:
             raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
 
+    def _check_gate_buffers(self, bias, routing, probs):
+        if bias is not None:
+            _check_rows(bias, "bias", (self.E,), _F32)
+        shape = self._routing_shape()
+        if routing is not None:
+            _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
+        if probs is not None:
+            _check_rows(probs, "probs", shape, _F32)
+
+    def _check_gate_options(self, bias=None, *, score="softmax", normalize=False, scale=1.0, routing=None, probs=None):
+        """What gate() refuses of its keyword arguments, for calls that have no logits yet."""
+        if score not in _SCORE:
+            raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+        _need(math.isfinite(scale), "scale must be finite")
+        self._check_gate_buffers(bias, routing, probs)
+        for name, t in (("bias", bias), ("routing", routing), ("probs", probs)):
+            if t is not None:
+                self._dev(t, name)
+        _check_aligned(routing=routing)
+
     def gate(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, *, score: str = "softmax",
              normalize: bool = False, scale: float = 1.0, routing: Optional[torch.Tensor] = None,
              probs: Optional[torch.Tensor] = None):
@@ -436,17 +464,12 @@ class Dispatcher:
         steers the choice only; -inf logits switch experts off.  Logits and
         routing start at a multiple of 16 bytes."""
         self._check_gate(logits, score)
-        if bias is not None:
-            _check_rows(bias, "bias", (self.E,), _F32)
+        self._check_gate_buffers(bias, routing, probs)
         shape = self._routing_shape()
         if routing is None:
             routing = torch.empty(shape, dtype=_ROUTING_OUT[self.route_fmt], device=self.device)
-        else:
-            _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
         if probs is None:
             probs = torch.empty(shape, dtype=torch.float32, device=self.device)
-        else:
-            _check_rows(probs, "probs", shape, _F32)
         _check_current_device((("logits", logits), ("bias", bias), ("routing", routing), ("probs", probs)))
         A.check(A.lib().moe_gate(C.byref(self.h), _ptr(logits), _ROW_DT[logits.dtype], _ptr(bias), _SCORE[score],
                                  1 if normalize else 0, float(scale), _ptr(routing), _ptr(probs), _stream()),
@@ -1046,6 +1069,49 @@ class Dispatcher:
                 "moe_decode_fused_fp8")
         return out
 
+    def _check_layer(self, x, routing, probs, w1, w2, w1_scales, w2_scales, T_live, router, gate, perm, perm_scales,
+                     scratch, expert_out, out):
+        """Whatever the layer's steps behind the norm check that does not wait
+        for the router's logits.  Returns the five buffers, those that the
+        caller omits allocated."""
+        _need(tuple(x.shape) == (self.T, self.H), f"x shape {tuple(x.shape)} != {(self.T, self.H)}")
+        if router is not None:
+            self._check_gate_options(**(gate or {}))
+            if T_live is not None:
+                self._dev(T_live, "T_live")
+                _need(T_live.dtype == torch.int32 and T_live.numel() == 1, "T_live must be one int32")
+        else:
+            _need(routing is not None, "the layer needs routing or a router")
+            self._check_routing(routing, probs, T_live)
+            _check_aligned(routing=routing)
+        F, wdtype = self._check_w1(w1, w1_scales)
+        F2, wdtype2 = self._check_w2(w2, w2_scales)
+        _need(F2 == F and wdtype2 == wdtype, "w1 and w2 must share the FFN width and dtype")
+        if wdtype == "bf16":
+            _need(self.H % 256 == 0 and F % 128 == 0, "bf16 weights need H % 256 == 0 and F % 128 == 0")
+        elif wdtype == "int4":
+            self._check_here()
+        fp8 = self.payload == A.FP8E4M3_B128
+        _need(not fp8 or wdtype == "fp8", "e4m3 rows need fp8 weights")
+        if perm is None:
+            perm = torch.empty((self.R, self.H), dtype=torch.float8_e4m3fn if fp8 else torch.bfloat16,
+                               device=self.device)
+        if fp8 and perm_scales is None:
+            perm_scales = torch.empty((self.R, self.H // 128), dtype=torch.float32, device=self.device)
+        self._check_perm(perm, perm_scales)
+        if scratch is None:
+            scratch = self.alloc_mlp_scratch(F, wdtype)
+        self._check_scratch(scratch, F, wdtype)
+        if expert_out is None:
+            expert_out = torch.empty((self.R, self.H), dtype=torch.bfloat16, device=self.device)
+        self._check_expert_out(expert_out)
+        if out is None:
+            out = torch.empty((self.T, self.H), dtype=torch.bfloat16, device=self.device)
+        self._dev(out, "out")
+        _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (self.T, self.H), "out must be bf16 [T,H]")
+        _check_aligned(w1=w1, w2=w2, perm=perm, scratch=scratch, expert_out=expert_out, out=out)
+        return perm, perm_scales, scratch, expert_out, out
+
     def layer(self, x, routing, probs, w1, w2, *, perm=None, perm_scales=None, scratch=None, expert_out=None,
               out=None, w1_scales=None, w2_scales=None, T_live=None, apply_probs=True, check_overflow=False,
               norm=None, router=None, gate=None, rms=None, residual=None):
@@ -1053,9 +1119,12 @@ class Dispatcher:
         ``norm`` = (weight, bias) or (weight, bias, eps), the layer reads
         layer_norm(x) in bf16 in place of x.  With ``rms`` = (weight,) or
         (weight, eps), it reads rms_norm(x + residual), and ``residual`` (if
-        given) becomes x + residual; with a handle of fp8 payload the norm
-        writes the codes that the dispatch takes, and bf16 rows for the
-        router alone.  With ``router``, a callable that takes the
+        given) becomes x + residual in every row, those from T_live on among
+        them; with a handle of fp8 payload the norm writes the codes that the
+        dispatch takes, and bf16 rows for the router alone.  A call that is
+        refused leaves ``residual`` as it was, unless it is refused for what
+        the router raised or returned: the router reads the norm's rows, and
+        the sum has been written with them.  With ``router``, a callable that takes the
         rows the layer reads and returns their logits [T,E], routing and probs
         (None then) are ``self.gate`` of those logits, with the keyword
         arguments ``gate`` (bias, score, normalize, scale).  With a
@@ -1073,6 +1142,10 @@ class Dispatcher:
         if norm is not None:
             x, _, _ = layer_norm(x, *norm, out_dtype=torch.bfloat16)
         elif rms is not None:
+            if residual is not None:
+                perm, perm_scales, scratch, expert_out, out = self._check_layer(
+                    x, routing, probs, w1, w2, w1_scales, w2_scales, T_live, router, gate, perm, perm_scales, scratch,
+                    expert_out, out)
             fp8 = self.payload == A.FP8E4M3_B128
             rows = router is not None or not fp8
             normed = rms_norm(x, *rms, residual=residual, total=residual, want_rows=rows, quantize=fp8,
