@@ -15,13 +15,14 @@
 // prologue, barriers and epilogue fall into the other's products.  Both operands
 // go straight to LDS, in stages of 32 elements of the sum (a ring of three or
 // four), the last step of a stage is multiplied behind the next stage's barrier.
-// Tiles of 256 features x 128 rows where they fill the CUs, else of 128 x 128
-// with four stages: such calls are bound by the latency of a stage (0.6 us), not
-// by bandwidth.  Measured on MI355X: 16 tokens, 256 experts top-8, 7168 x 4096
-// transposed 1.04 ms (5.7 TB/s of the touched weights); one token 85 to 91 us (5.1
-// to 5.5 TB/s; 138 us with the wide tiles); 3001 tokens over 60 experts, 2056 x
-// 1416, 134 us (510 TFLOP/s); the weight's gradient of 1501 tokens over 24
-// experts, 1048 x 904, fp32 and added, 79 us.
+// Tiles of 256 features x 128 rows, or of 128 x 128 with four stages where those
+// go into fewer rounds (narrow below): such calls are bound by the latency of a
+// stage (0.6 us), not by bandwidth.  Measured on MI355X: 16 tokens, 256 experts
+// top-8, 7168 x 4096 transposed 1.02 ms (5.8 TB/s of the touched weights); one
+// token 85 to 91 us (5.1 to 5.5 TB/s; 138 us with the tiles of 256 features);
+// 2048 tokens over the same experts, transposed, 2.82 ms (5.5 TB/s).  The weight's
+// gradient of 1501 tokens over 24 experts, 1048 x 904: bf16 31 us, added 56, fp32
+// 43, added 79; of 1024 rows over 32 experts, 4096 x 7168, 304 us (6.2 TB/s).
 //
 // An expert's rows are cut into tiles of nearly one size and each XCD takes one
 // contiguous run of the tiles, so that the tiles that share an expert's rows and
@@ -365,6 +366,10 @@ long long copies(const moe_handle* h) { return (long long)h->desc.T * h->desc.K;
 //   rows (128 wide tiles for 256 CUs) 23 and 27
 //   weights, 64 experts, 4096 x 7168: 8 rows 620 and 730, 64 rows 760 and 710, 512 rows 2600 and 2120; 32 experts,
 //   1024 x 2048 (1024 wide tiles), 1024 rows 148 and 139; 24 experts, 1048 x 904 (480 wide tiles) 78 and 105
+// The mean also stands for uneven rows.  With an offset per expert of standard
+// deviation 3 in the router's logits, us in the small and the wide tiles, 7168 -> 4096 transposed: 32
+// experts, 512 tokens top-8, 448 and 478 (even: 487 and 436), 4096 tokens 2015 and
+// 1869 (1944 and 1750); 256 experts, 2048 tokens, 2320 and 2612 (2819 and 3163).
 bool wide_rows(const moe_handle* h, int na, int width, int num_cu) {
     const long long rows = copies(h) / h->desc.E;
     return rows >= 96 && h->desc.E * ceil_div(rows, 256) * ceil_div(na, width) >= num_cu;
@@ -385,10 +390,21 @@ bool narrow(long long tiles, int features, int width, int num_cu) {
 }
 // Weights that are not read across, streamed for few rows: the expert MLP's FC2
 // kernel, which takes a unit's rows all at once and keeps two stages of weights
-// in registers on their way.  256 experts, 7168 x 4096, against the better of the
-// two above: 16 tokens 1010 and 1100 us, 64 rows each 2740 and 2990, 256 rows
-// 4110 and 4850, 512 rows 8780 and 7610.  Below some hundred MB of weights it
-// has too few units: 32 experts, 2048 x 2048, 1 to 64 rows 47 to 76 and 38 to 72.
+// in registers on their way.  us of it and of the better of the two above:
+//   256 experts, 7168 -> 4096: 16 tokens 1010 and 1100, 64 rows each 2740 and 2990, 256 rows 4110 and 4850, 512 rows
+//   8780 and 7610
+//   7168 -> 4096, 1, 16, 64 and 256 rows each: 64 experts (3.8 GB) 406 606 656 1045 and 447 666 713 1179; 32 experts
+//   (512 units) 259 298 325 562 and 270 335 377 604; 16 experts (256 units, left to the others) 131 155 165 323 and
+//   143 174 186 372; 8 experts (128 units) 125 126 117 157 and 85 87 96 167
+//   2048 -> 7168, the same rows: 64 experts (1.9 GB) 220 371 403 562 and 219 340 362 612; 32 experts 141 206 225 307
+//   and 134 195 207 344; 16 experts (448 units, left to the others) 94 105 116 177 and 78 101 110 178
+//   1024 -> 7168: 64 experts (0.9 GB) 114 179 194 309 and 108 171 202 330; 32 experts (0.5 GB) 71 99 110 171 and 63 91
+//   106 185; 16 experts (0.2 GB, left to the others) 50 53 60 101 and 39 47 57 98
+//   32 experts, 2048 x 2048 (0.3 GB), 1 to 64 rows 47 to 76 and 38 to 72
+// Nearer to the border either side is up to 13 % ahead.  Uneven rows cost it more
+// than the others: beyond 320 rows of an expert the weights are streamed again.
+// 7168 -> 4096 with the offsets above: 32 experts, 512 tokens, 622 and 546 (even:
+// 366 and 406); 256 experts, 2048 tokens, 3496 and 2626 (2555 and 2808).
 bool stream_weights(const moe_handle* h, int N, int M, int num_cu) {
     const long long touched = copies(h) < h->desc.E ? copies(h) : h->desc.E;
     return N % 256 == 0 && M % 128 == 0 && copies(h) <= 320ll * h->desc.E && touched * N * M * 2 > (384ll << 20) &&

@@ -11,16 +11,19 @@
 // wait for those.  The tile's second stage does: its wait counts stores like
 // transfers, and they were issued before it.  They have one stage's time then,
 // which long sums do not notice; with the four or five stages of a weight's
-// gradient of 256 rows the stores' 2.2 us show.  Up to eight tiles of rows take a feature tile one after the
-// other: an expert's weights are then read from HBM once (32 experts of 1000
-// rows: 8, 4 and 2 tiles together 1761, 1787 and 1884 us).
+// gradient of 256 rows the stores' 2.2 us show.  Up to eight tiles of rows take
+// a feature tile one after the other: an expert's weights are then read from HBM
+// once (32 experts of 1000 rows: 8, 4 and 2 tiles together 1761, 1787 and 1884
+// us).
 //
 // Measured on MI355X: 32768 rows over 32 experts, 7168 x 4096, 1.72 ms (1120
 // TFLOP/s; transposed 1.71), its weight's gradient 1.44 ms, [256,7168,2048] of
-// 65536 rows 2.80 ms (7.5 GB written); one expert, 8192 x 8192 x 8192, 0.86 ms
-// (1270 TFLOP/s, where a library product of that size reaches 1445).  The
-// matrix pipe is busy 47 to 64 % of the cycles at the 1.9 to 2.1 GHz that the chip
-// holds: a stage of 2048 matrix cycles takes 3300, of which the waits for its
+// 65536 rows 2.80 ms (7.5 GB written); 11804 rows over 60 uneven experts, 2056 x
+// 1416 transposed, 134 to 142 us (505 TFLOP/s; the tiles of 256 x 128 take 141);
+// one expert, 8192 x 8192 x 8192, 0.86 ms (1270 TFLOP/s, where a library product
+// of that size reaches 1445).  The matrix pipe is busy 46 to 59 % of the cycles
+// in the sizes of 32 experts (31 % in the weight's gradient of 256 rows each) at
+// the 1.9 to 2.2 GHz that the chip holds: a stage of 2048 matrix cycles takes 3300, of which the waits for its
 // transfers are 2 to 4 %.  With transfers that always hit L2 it takes 83 % of
 // that, without transfers in the loop 72 %.
 #include "grouped.h"
