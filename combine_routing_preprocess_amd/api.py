@@ -435,24 +435,22 @@ class Dispatcher:
         if score not in _SCORE:
             raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
 
-    def _check_gate_buffers(self, bias, routing, probs):
-        if bias is not None:
-            _check_rows(bias, "bias", (self.E,), _F32)
-        shape = self._routing_shape()
-        if routing is not None:
-            _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
-        if probs is not None:
-            _check_rows(probs, "probs", shape, _F32)
-
     def _check_gate_options(self, bias=None, *, score="softmax", normalize=False, scale=1.0, routing=None, probs=None):
         """What gate() refuses of its keyword arguments, for calls that have no logits yet."""
         if score not in _SCORE:
             raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
-        _need(math.isfinite(scale), "scale must be finite")
-        self._check_gate_buffers(bias, routing, probs)
-        for name, t in (("bias", bias), ("routing", routing), ("probs", probs)):
+        _need(math.isfinite(C.c_float(scale).value), "scale must be finite in fp32")
+        shape = self._routing_shape()
+        spans = []
+        for name, t, want, dtypes in (("bias", bias, (self.E,), _F32), ("probs", probs, shape, _F32),
+                                      ("routing", routing, shape, _FMT_DTYPES[self.route_fmt])):
             if t is not None:
-                self._dev(t, name)
+                _check_rows(t, name, want, dtypes)
+                if self._cuda:
+                    _check_current_device(((name, t),))
+                spans.append((t.data_ptr(), t.data_ptr() + _nbytes(t)))
+        _need(all(a[1] <= b[0] or b[1] <= a[0] for i, a in enumerate(spans) for b in spans[:i]),
+              "bias, routing and probs must not overlap")
         _check_aligned(routing=routing)
 
     def gate(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, *, score: str = "softmax",
@@ -464,12 +462,17 @@ class Dispatcher:
         steers the choice only; -inf logits switch experts off.  Logits and
         routing start at a multiple of 16 bytes."""
         self._check_gate(logits, score)
-        self._check_gate_buffers(bias, routing, probs)
+        if bias is not None:
+            _check_rows(bias, "bias", (self.E,), _F32)
         shape = self._routing_shape()
         if routing is None:
             routing = torch.empty(shape, dtype=_ROUTING_OUT[self.route_fmt], device=self.device)
+        else:
+            _check_rows(routing, "routing", shape, _FMT_DTYPES[self.route_fmt])
         if probs is None:
             probs = torch.empty(shape, dtype=torch.float32, device=self.device)
+        else:
+            _check_rows(probs, "probs", shape, _F32)
         _check_current_device((("logits", logits), ("bias", bias), ("routing", routing), ("probs", probs)))
         A.check(A.lib().moe_gate(C.byref(self.h), _ptr(logits), _ROW_DT[logits.dtype], _ptr(bias), _SCORE[score],
                                  1 if normalize else 0, float(scale), _ptr(routing), _ptr(probs), _stream()),

@@ -101,11 +101,15 @@ def test_bf16_weights_of_an_odd_width_refused_before_the_norm():
                 residual=torch.zeros(T, h, dtype=BF))
 
 
+_SHARED = torch.zeros(4 * T * K, dtype=torch.uint8)
 GATE = {
     "gate score": dict(score="tanh"),
     "gate option": dict(temperature=2.0),
     "gate scale": dict(scale=float("inf")),
+    "gate scale in fp32": dict(scale=1e39),
     "gate bias": dict(bias=torch.zeros(E + 1)),
+    "gate routing over probs": dict(routing=_SHARED[:2 * T * K].view(torch.int16).view(T, K),
+                                    probs=_SHARED.view(torch.float32).view(T, K)),
     "gate routing": dict(routing=torch.zeros(T, K, dtype=torch.int32)),
     "gate routing at an odd address": dict(routing=_off_by(torch.zeros(T, K, dtype=torch.int16), 2)),
     "gate probs": dict(probs=torch.zeros(T, K + 1)),
