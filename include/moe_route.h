@@ -536,8 +536,8 @@ int moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t y_dty
  * output's type.  Rows that hold no kept copy are neither read nor written.
  * Rows are bf16 whatever the handle's payload; the handle needs routing
  * metadata.  Common requirements: N, M, H, F multiples of 8, from 8 to
- * MOE_GROUPED_MAX (2 F too), N * M and 2 F * H <= 2^30 (MOE_ESHAPE); arrays 16-byte aligned; outputs
- * overlap neither inputs nor each other (MOE_EINVAL). */
+ * MOE_GROUPED_MAX (2 F too), N * M and 2 F * H <= 2^30 (MOE_ESHAPE); arrays
+ * 16-byte aligned; outputs overlap neither inputs nor each other (MOE_EINVAL). */
 #define MOE_GROUPED_MAX 65536
 
 /* out_r = w_e rows_r, or with `transpose` out_r = w_e^T rows_r (the gradient of
